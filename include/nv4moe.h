@@ -469,4 +469,6 @@ nv4_status moe_combine(const void *Y, nv4_dtype ytype, int64_t ldy, const int32_
 }
 #endif
 
+#include "nv4moe/mxfp4.h" /* the MXFP4 calls */
+
 #endif /* NV4MOE_H */

@@ -18,6 +18,9 @@ forward (route, quantise, permute, GEMM + SwiGLU, quantise, GEMM, combine) and
 its four backward grouped GEMMs.  ``moe_forward_bf16`` is the unquantised layer
 and ``moe_backward_bf16`` the backward on BF16 operands: the forward's NVFP4
 tensors dequantised (the dequantized backward) or the BF16 tensors themselves.
+The MXFP4 calls (mxfp4_quantize, mxfp4_dequantize, mxfp4_grouped_gemm, the layer
+mx_moe_forward / mx_moe_backward and its decode form mx_moe_few) are in mxfp4.py and
+reachable from here.
 There is no fallback: if the library is not built, every call raises.
 """
 
@@ -918,3 +921,8 @@ def nv4_bench_lds(out: torch.Tensor | None, iters: int, stream=None) -> tuple:
         out = torch.empty(n, dtype=torch.int32, device="cuda")
     _check(lib.nv4_bench_lds(_ptr(out), iters, _stream(stream)))
     return out, n * iters * 8 * 16
+
+
+# ----------------------------------------------------------------------------- MXFP4
+
+from .mxfp4 import *  # noqa: E402,F401,F403  (needs the names above)

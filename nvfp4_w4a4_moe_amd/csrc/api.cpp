@@ -10,11 +10,14 @@
 #include <mutex>
 
 #include "../../include/nv4moe.h"
+#include "api_common.h"
 #include "nv4_internal.h"
 
-namespace {
+namespace nv4 {
 
+namespace {
 thread_local char g_err[512] = "no error";
+}
 
 nv4_status fail(nv4_status s, const char *fmt, ...) {
   va_list ap;
@@ -34,9 +37,15 @@ nv4_status from_hip(hipError_t e, const char *what) {
   return fail(NV4_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace nv4
 
-size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+using nv4::aligned;
+using nv4::fail;
+using nv4::from_hip;
+using nv4::ok;
+using nv4::round256;
+
+namespace {
 
 int ngroups_of(int64_t rows, int scale_mode, int nseg) {
   if (scale_mode == NV4_SCALE_TENSOR) return 1;
@@ -81,7 +90,7 @@ const char *nv4_status_string(nv4_status s) {
   return "unknown status";
 }
 
-const char *nv4_last_error(void) { return g_err; }
+const char *nv4_last_error(void) { return nv4::g_err; }
 
 // ---------------------------------------------------------------- quantisation
 
@@ -584,7 +593,7 @@ nv4_status nv4_to_bf16(const void *x, int64_t x_rows, int64_t ldx, const nv4_ten
     if (!row_index && q->rows != rows) return fail(NV4_EINVAL, "nv4_to_bf16: q->rows != rows");
     if (row_index && rows > 0 && q->rows <= 0) return fail(NV4_EINVAL, "nv4_to_bf16: row index into an empty q");
     if (q->scale_mode == NV4_SCALE_SEGMENT && (q->nseg <= 0 || q->rows % q->nseg))
-      return fail(NV4_EINVAL, "nv4_to_bf16: segment scales need q->rows % q->nseg == 0");
+      return fail(NV4_EINVAL, "nv4_to_bf16: segment scales need q->rows %% q->nseg == 0");
     if (q->scale_mode == NV4_SCALE_SEGMENT_HALVES)
       return fail(NV4_EUNSUPPORTED, "nv4_to_bf16: per-K-half scales are not supported as a source");
     if (q->scale_mode != NV4_SCALE_TENSOR && q->scale_mode != NV4_SCALE_SEGMENT && q->scale_mode != NV4_SCALE_ROW)

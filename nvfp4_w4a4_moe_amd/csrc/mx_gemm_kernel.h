@@ -1,0 +1,634 @@
+// Grouped MXFP4 x MXFP4 GEMM for gfx950: the kernel template and its launcher.
+//
+//   C[r][n] = sum over blocks b of 2^(ea[r][b] + eb[n][b]) * sum_i qa[r][b,i] qb[n][b,i]
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 computes exactly this on the stored bytes: a lane holds
+// the 32 codes (16 bytes) of one row's block and the block's E8M0 byte.  Nothing is decoded,
+// so the kernel moves 0.53 bytes per operand element from HBM to the matrix unit.  A loop of
+// this instruction alone reaches 8.1 PFLOP/s on this card (the 16x16x128 form 4.3).
+//
+// Operand roles.  With the rows of A (tokens) as the instruction's first operand a lane holds
+// one output column of 16 tokens: FP32 and BF16 rows leave as 128- and 64-byte pieces.  Where
+// the SwiGLU result is quantised (TRANS) the roles are swapped: a lane then holds 16 columns of
+// one token, and weight row n of a 32-row fragment sits at the operand row that makes them
+// consecutive (frag_row), so that an MX block is two lanes' registers.
+//
+// Data flow: HBM / L2 -> LDS by 16-byte DMA (stages of K = 128: 64 bytes of codes and 4 scale
+// bytes per row, a ring of kStages) -> registers (16-byte LDS reads, one per lane and
+// 64 K) -> MFMA.  In LDS, chunk q of row r sits at q ^ ((r >> 2) & 3): the 16 rows of one read
+// pass then cover all 64 banks.
+//
+// Pipeline.  Stage s of a tile lives in ring slot s mod kStages.  A stage is two K = 64 steps;
+// in the middle of a stage every wave waits for its own loads of the next one, the workgroup
+// meets, and the slot just read is refilled: with this tile's stage s + kStages, or, in the
+// tile's last kStages stages, with the next tile's stage of that slot, so that loads run
+// across tile ends and under the epilogue.  The next stage's first step is read while this
+// stage's second one multiplies.  Every stage issues the same number of loads (a load with
+// nothing to fetch has an offset behind the buffer) and every epilogue the same number of
+// branch-free stores, so a wait counts exactly what may still be under way.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "mx_device.h"
+#include "mx_internal.h"
+#include "nv4_internal.h"
+#include "../../include/nv4moe.h"
+
+// (lambdas that hold the accumulators by reference must be inlined for them to stay in registers)
+#define MX_INLINE __attribute__((always_inline))
+
+namespace nv4 {
+namespace {
+
+constexpr int kMxMaxExperts = 1024;
+constexpr int kMxXcds = 8;
+constexpr uint32_t kNoRow = 0xFFFFFF00u;  // a byte offset behind every buffer: loads return zeros
+
+template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES, int WAVES_PER_SIMD>
+struct MxTile {
+  static constexpr int kWavesM = WAVES_M, kWavesN = WAVES_N, kFM = FM, kFN = FN;
+  static constexpr int kStages = STAGES, kWavesPerSimd = WAVES_PER_SIMD;
+  static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
+  static constexpr int BM = WAVES_M * FM * 32;  // rows of A (tokens)
+  static constexpr int BN = WAVES_N * FN * 32;  // rows of B (weights)
+  static constexpr int kCodes = (BM + BN) * 64, kStageBytes = kCodes + (BM + BN) * 4;
+  static constexpr int kCodeBlocks = (BM + BN) / 16;           // 1 KB DMAs: 16 rows
+  static constexpr int kCodeDma = (kCodeBlocks + NW - 1) / NW;  // per wave; surplus ones repeat the last block
+  static constexpr int kScaleBlocks = (BM + BN + 63) / 64;     // 256-byte DMAs: 64 rows
+  static constexpr int kScaleDma = (kScaleBlocks + NW - 1) / NW;
+  static constexpr int kDma = kCodeDma + kScaleDma;  // the same for every wave
+  static_assert((BM + BN) % 64 == 0, "whole scale blocks");
+};
+
+typedef __attribute__((address_space(3))) void *mx_lds_ptr;
+__device__ __forceinline__ void mx_dma16(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst,
+      16, voff, 0, 0, 0);
+}
+__device__ __forceinline__ void mx_dma4(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 4,
+      voff, 0, 0, 0);
+}
+
+// wait until at most N vector-memory operations of this wave are outstanding
+template <int N>
+__device__ __forceinline__ void mx_wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+// wait for this wave's LDS operations (lgkmcnt(0) only)
+__device__ __forceinline__ void mx_wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+}
+
+// workgroup barrier without a memory fence (which would drain the prefetches)
+__device__ __forceinline__ void mx_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Branch-free stores into [base, base + bytes) at byte offset voff; an offset of kNoStore is
+// dropped.  base is the same for the whole wave.
+constexpr uint32_t kNoStore = 0x80000000u;
+__device__ __forceinline__ void *mx_uniform_ptr(const void *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<void *>(((uint64_t)hi << 32) | lo);
+}
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void mx_store8(void *base, uint32_t bytes, uint32_t voff, uint32_t a, uint32_t b) {
+  __builtin_amdgcn_raw_buffer_store_b64(
+      u32x2{a, b},
+      __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000), voff,
+      0, 0);
+}
+__device__ __forceinline__ void mx_store4(void *base, uint32_t bytes, uint32_t voff, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b32(
+      v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000), voff,
+      0, 0);
+}
+__device__ __forceinline__ void mx_store2(void *base, uint32_t bytes, uint32_t voff, uint16_t v) {
+  __builtin_amdgcn_raw_buffer_store_b16(
+      v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000), voff,
+      0, 0);
+}
+__device__ __forceinline__ void mx_store1(void *base, uint32_t bytes, uint32_t voff, uint32_t b) {
+  __builtin_amdgcn_raw_buffer_store_b8(
+      (uint8_t)b,
+      __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000), voff,
+      0, 0);
+}
+
+__device__ __forceinline__ int64_t mx_uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// An LDS dword that no load in flight can change, read without the compiler's wait for those
+// loads (it cannot tell the tables from the ring); the wait for the value is in the block.
+__device__ __forceinline__ int mx_table(const int *p) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(v)
+               : "v"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) int *)p)
+               : "memory");
+  return v;
+}
+
+// TRANS: weight row (within its 32-row fragment) at operand row i.  Accumulator register r of
+// lane half h holds operand row 8 (r / 4) + 4 h + r % 4; it shall be column 16 h + r.
+__device__ __forceinline__ int frag_row(int i) { return ((i >> 2) & 1) * 16 + (i >> 3) * 4 + (i & 3); }
+
+// gate / (1 + exp(-gate)) * up in FP32 (hardware exp2 and reciprocal, relative error ~1e-7)
+__device__ __forceinline__ float mx_swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+struct MxJob {
+  int e, nt;
+  int64_t m0, m_end;   // rows of A / C
+  int64_t k_lo, k_hi;  // contraction range
+  int nst;             // stages
+};
+
+template <class Cfg, int GROUP, int EPI>
+struct MxTiles {
+  // The workgroup's sequence of tiles.  GROUP_M: logical tiles in XCD order (workgroup i runs
+  // on XCD i % 8): the workgroups of one XCD take consecutive tiles, which share A rows and
+  // an expert's weights in its L2.  GROUP_K: experts by decreasing length and the tiles dealt
+  // out in turn, forwards then backwards, so that every workgroup gets long and short ones.
+  const MxGemmArgs &g;
+  const int *off;  // the expert offsets
+  const int *tab;  // GROUP_M: first M tile of each expert; GROUP_K: experts by length
+  int64_t total;
+  int ntn;
+  __device__ int64_t index(int64_t it) const {  // grows with it
+    const int64_t G = gridDim.x;
+    if (GROUP == NV4_GROUP_K) return it * G + ((it & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+    const int64_t per = G / kMxXcds;
+    const int64_t slot = blockIdx.x < per * kMxXcds ? (blockIdx.x % kMxXcds) * per + blockIdx.x / kMxXcds : blockIdx.x;
+    return it * G + slot;
+  }
+  __device__ bool has(int64_t it) const { return index(it) < total; }
+  __device__ MxJob get(int64_t it) const {
+    MxJob j;
+    const int64_t L = index(it);
+    if (GROUP == NV4_GROUP_M) {
+      const int mt = (int)(L / ntn);
+      j.nt = (int)(L - (int64_t)mt * ntn);
+      // last expert with tab[e] <= mt (it owns at least one tile); tab does not decrease
+      int n = 0;
+      for (int e = 0; e < g.E; e += 64) {
+        const int i = e + (threadIdx.x & 63);
+        n += __popcll(__ballot(i < g.E && mx_table(tab + min(i, g.E)) <= mt));
+      }
+      j.e = n - 1;
+      j.m0 = (int64_t)mx_table(off + j.e) + (int64_t)(mt - mx_table(tab + j.e)) * Cfg::BM;
+      j.m_end = std::min<int64_t>(mx_table(off + j.e + 1), g.M_cap);
+      j.k_lo = 0;
+      j.k_hi = g.K;
+    } else {
+      const int tn = (int)((g.a_rows + Cfg::BM - 1) / Cfg::BM);
+      const int per_e = tn * ntn;
+      const int rank = (int)(L / per_e), r = (int)(L - (int64_t)rank * per_e);
+      j.e = mx_table(tab + rank);
+      j.nt = r % ntn;
+      j.m0 = (int64_t)(r / ntn) * Cfg::BM;
+      j.m_end = g.a_rows;
+      j.k_lo = std::min<int64_t>(mx_table(off + j.e), g.K);
+      j.k_hi = std::max<int64_t>(std::min<int64_t>(mx_table(off + j.e + 1), g.K), j.k_lo);
+    }
+    j.e = __builtin_amdgcn_readfirstlane(j.e);
+    j.nt = __builtin_amdgcn_readfirstlane(j.nt);
+    j.m0 = mx_uniform(j.m0);
+    j.m_end = mx_uniform(j.m_end);
+    j.k_lo = mx_uniform(j.k_lo);
+    j.k_hi = mx_uniform(j.k_hi);
+    j.nst = (int)((j.k_hi - j.k_lo + 127) / 128);
+    return j;
+  }
+};
+
+// Row of B for tile row r, or -1 behind the matrix.  SwiGLU: a wave's fragments are FN/2 of
+// gate rows, then the up rows of the same columns.
+template <class Cfg, int GROUP, int EPI, bool TRANS>
+__device__ __forceinline__ int64_t mx_b_row(const MxGemmArgs &g, const MxJob &j, int r) {
+  const int in = TRANS ? (r & ~31) | frag_row(r & 31) : r;
+  if (GROUP == NV4_GROUP_K) {
+    const int64_t col = (int64_t)j.nt * Cfg::BN + in;
+    return col < g.b_rows ? col : -1;
+  }
+  if (EPI == NV4_EPI_SWIGLU) {
+    constexpr int half = Cfg::kFN / 2;
+    const int wv = in / (Cfg::kFN * 32), f = (in / 32) % Cfg::kFN;
+    const int64_t col = (int64_t)j.nt * (Cfg::BN / 2) + wv * (half * 32) + (f % half) * 32 + (in & 31);
+    return col < g.N ? ((int64_t)j.e * 2 + (f >= half ? 1 : 0)) * g.N + col : -1;
+  }
+  const int64_t col = (int64_t)j.nt * Cfg::BN + in;
+  return col < g.N ? (int64_t)j.e * g.N + col : -1;
+}
+
+template <class Cfg, int GROUP, int EPI, bool OUT_F32, bool TRANS>
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::kWavesPerSimd)))
+void k_mx_gemm(MxGemmArgs g) {
+  constexpr int BM = Cfg::BM, BN = Cfg::BN, FM = Cfg::kFM, FN = Cfg::kFN, NT = Cfg::NT, S = Cfg::kStages;
+  constexpr bool SWIGLU = EPI == NV4_EPI_SWIGLU;
+  static_assert(!TRANS || SWIGLU, "the quantised result is the SwiGLU's");
+  // the ring's slots are separate arrays and every access names its slot at compile time: the
+  // compiler then knows that the reads of one slot do not depend on the loads into another
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[Cfg::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring1[Cfg::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring2[S > 2 ? Cfg::kStageBytes : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring3[S > 3 ? Cfg::kStageBytes : 16];
+  static_assert(S >= 2 && S <= 4, "ring of 2 to 4 slots");
+  __shared__ int tab[kMxMaxExperts + 1];
+  __shared__ int off[kMxMaxExperts + 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / Cfg::kWavesN, wn = wave % Cfg::kWavesN;
+  const int h = lane >> 5, l32 = lane & 31;
+  const int64_t ld = g.K / 2, sld = (g.K / kMxBlock + 3) / 4 * 4;
+  const uint32_t a_bytes = (uint32_t)(g.a_rows * ld), a_sbytes = (uint32_t)(g.a_rows * sld);
+  const uint32_t b_bytes = (uint32_t)(g.b_rows * ld), b_sbytes = (uint32_t)(g.b_rows * sld);
+
+  // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty)
+  for (int e = tid; e <= g.E; e += NT) off[e] = std::max(g.offsets[e], 0);
+  __syncthreads();
+  MxTiles<Cfg, GROUP, EPI> tiles{g, off, tab, 0, 0};
+  if (GROUP == NV4_GROUP_M) {
+    int *scratch = reinterpret_cast<int *>(ring0);
+    const int per = (g.E + NT - 1) / NT;
+    int own = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e < g.E) own += (std::max(off[e + 1] - off[e], 0) + BM - 1) / BM;
+    }
+    scratch[tid] = own;
+    __syncthreads();
+    for (int o = 1; o < NT; o <<= 1) {
+      const int x = tid >= o ? scratch[tid - o] : 0;
+      __syncthreads();
+      scratch[tid] += x;
+      __syncthreads();
+    }
+    int run = scratch[tid] - own;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e < g.E) {
+        tab[e] = run;
+        run += (std::max(off[e + 1] - off[e], 0) + BM - 1) / BM;
+      }
+    }
+    if (tid == NT - 1) tab[g.E] = scratch[tid];
+    __syncthreads();
+    constexpr int cols = SWIGLU ? BN / 2 : BN;
+    tiles.ntn = (int)((g.N + cols - 1) / cols);
+    tiles.total = mx_uniform((int64_t)tab[g.E] * tiles.ntn);
+  } else {
+    for (int e = tid; e < g.E; e += NT) {
+      const int n = off[e + 1] - off[e];
+      int rank = 0;
+      for (int f = 0; f < g.E; ++f) {
+        const int m = off[f + 1] - off[f];
+        rank += (m > n) || (m == n && f < e);
+      }
+      tab[rank] = e;
+    }
+    __syncthreads();
+    tiles.ntn = (int)((g.b_rows + BN - 1) / BN);
+    tiles.total = (int64_t)g.E * ((g.a_rows + BM - 1) / BM) * tiles.ntn;
+  }
+
+  // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included)
+  uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
+  const int qrow = lane >> 2, qpos = lane & 3;
+  int64_t p_it = 0;  // the loading tile
+  MxJob pj{};
+  bool p_live;  // there is one
+  const auto p_setup = [&]() MX_INLINE {
+#pragma unroll
+    for (int i = 0; i < Cfg::kCodeDma; ++i) {
+      const int b = std::min(wave * Cfg::kCodeDma + i, Cfg::kCodeBlocks - 1);
+      const int r = b * 16 + qrow;
+      int64_t row;
+      if (r < BN) {
+        row = mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
+      } else {
+        row = pj.m0 + (r - BN);
+        if (row >= pj.m_end) row = -1;
+        else if (GROUP == NV4_GROUP_M && g.a_rows_index) row = min((int64_t)max(g.a_rows_index[row], 0), g.a_rows - 1);
+      }
+      off_c[i] = row < 0 ? kNoRow : (uint32_t)(row * ld) + (uint32_t)((qpos ^ ((r >> 2) & 3)) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < Cfg::kScaleDma; ++i) {
+      const int b = std::min(wave * Cfg::kScaleDma + i, Cfg::kScaleBlocks - 1);
+      const int r = b * 64 + lane;
+      int64_t row;
+      if (r < BN) {
+        row = mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
+      } else {
+        row = pj.m0 + (r - BN);
+        if (row >= pj.m_end) row = -1;
+        else if (GROUP == NV4_GROUP_M && g.a_rows_index) row = min((int64_t)max(g.a_rows_index[row], 0), g.a_rows - 1);
+      }
+      off_s[i] = row < 0 ? kNoRow : (uint32_t)(row * sld);
+    }
+  };
+  // loading tile: the first one from p_it on with at least one stage (GROUP_K: an empty
+  // range has none)
+  const auto p_find = [&]() MX_INLINE {
+    p_live = false;
+    while (tiles.has(p_it)) {
+      pj = tiles.get(p_it);
+      if (pj.nst > 0) {
+        p_live = true;
+        p_setup();
+        break;
+      }
+      ++p_it;
+    }
+  };
+  // one stage of the loading tile into a ring slot (live: there is such a stage)
+  const auto load_stage = [&](uint8_t *dst, int p_st, bool live) MX_INLINE {
+    const uint32_t kc = (uint32_t)((pj.k_lo + (int64_t)p_st * 128) / 2), ks = kc / 16;
+    // elements of this stage (may exceed 128)
+    const int left = live ? (int)((pj.k_hi - pj.k_lo) - (int64_t)p_st * 128) : 0;
+#pragma unroll
+    for (int i = 0; i < Cfg::kCodeDma; ++i) {
+      const int b = std::min(wave * Cfg::kCodeDma + i, Cfg::kCodeBlocks - 1);
+      const bool in_k = (int)((qpos ^ (((b * 16 + qrow) >> 2) & 3)) * 32) < left;
+      const uint32_t v = (off_c[i] == kNoRow || !in_k) ? kNoRow : off_c[i] + kc;
+      const bool isb = b * 16 < BN;
+      mx_dma16(isb ? g.b_codes : g.a_codes, isb ? b_bytes : a_bytes, dst + b * 1024, v);
+    }
+#pragma unroll
+    for (int i = 0; i < Cfg::kScaleDma; ++i) {
+      const int b = std::min(wave * Cfg::kScaleDma + i, Cfg::kScaleBlocks - 1);
+      const uint32_t v = (off_s[i] == kNoRow || left <= 0) ? kNoRow : off_s[i] + ks;
+      const bool isb = b * 64 < BN;
+      mx_dma4(isb ? g.b_scales : g.a_scales, isb ? b_sbytes : a_sbytes, dst + Cfg::kCodes + b * 256, v);
+    }
+  };
+  static_assert(BN % 64 == 0, "scale blocks of one operand");
+
+  p_find();
+  load_stage(ring0, 0, p_live);
+  load_stage(ring1, 1, p_live);
+  if constexpr (S > 2) load_stage(ring2, 2, p_live);
+  if constexpr (S > 3) load_stage(ring3, 3, p_live);
+
+  // ---- fragments of one K = 64 step: chunk 2 step + h of the wave's rows
+  i32x8 wf[2][FN], tf[2][FM];
+  uint32_t ws[2][FN] = {}, ts[2][FM] = {};  // scale dwords shifted so that byte 0 is step 0's, byte 2 step 1's
+  const int w_row = wn * FN * 32 + l32, t_row = BN + wm * FM * 32 + l32;
+  const int sw = (l32 >> 2) & 3;  // the same for every fragment (rows differ by multiples of 32)
+  const auto read_codes = [&](const uint8_t *st, int step, i32x8 (&w)[FN], i32x8 (&t)[FM]) {
+    const int pos = ((2 * step + h) ^ sw) * 16;
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const int4 v = *reinterpret_cast<const int4 *>(st + (w_row + f * 32) * 64 + pos);
+      w[f] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const int4 v = *reinterpret_cast<const int4 *>(st + (t_row + f * 32) * 64 + pos);
+      t[f] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+    }
+  };
+  const auto read_scales = [&](const uint8_t *st, uint32_t (&w)[FN], uint32_t (&t)[FM]) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      w[f] = *reinterpret_cast<const uint32_t *>(st + Cfg::kCodes + (w_row + f * 32) * 4) >> (8 * h);
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+      t[f] = *reinterpret_cast<const uint32_t *>(st + Cfg::kCodes + (t_row + f * 32) * 4) >> (8 * h);
+  };
+
+  f32x16 acc[FN][FM];
+  const auto clear = [&]() MX_INLINE {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  };
+
+  // ---- a finished tile (!TRANS: exactly kStores stores)
+  constexpr int NF = SWIGLU ? FN / 2 : FN;  // 32-column fragments of the result
+  constexpr int ESZ = OUT_F32 ? 4 : 2;
+  constexpr int kStores = FM * NF * 16;
+  const auto finish = [&](const MxJob &j) MX_INLINE {
+    const int ncols = (int)(GROUP == NV4_GROUP_K ? g.b_rows : g.N);
+    const int col_w = j.nt * (SWIGLU ? BN / 2 : BN) + wn * NF * 32;  // this wave's first column
+    const int64_t row_w = j.m0 + wm * FM * 32;
+    const int rows = (int)std::min<int64_t>(std::max<int64_t>(j.m_end - row_w, 0), FM * 32);
+    const int ldc = (int)g.ldc;
+    char *cb = static_cast<char *>(g.C) + ((GROUP == NV4_GROUP_K ? (int64_t)j.e * g.a_rows : 0) + row_w) * g.ldc * ESZ;
+    if constexpr (!TRANS) {
+      // lane = column l32 of a fragment; registers: rows 8 (r / 4) + 4 h + r % 4
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int g4 = 0; g4 < 4; ++g4) {
+          // the group's 8 rows: a store behind the valid ones falls behind the buffer
+          const int r0 = i * 32 + g4 * 8;
+          const uint32_t nb = (uint32_t)(std::min(std::max(rows - r0, 0), 8) * ldc * ESZ);
+          void *rb = mx_uniform_ptr(cb + (int64_t)r0 * ldc * ESZ);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+              const int col = col_w + f * 32 + l32;
+              const uint32_t v = col < ncols ? (uint32_t)(((q + h * 4) * ldc + col) * ESZ) : kNoStore;
+              float x = acc[f][i][g4 * 4 + q];
+              if constexpr (SWIGLU) x = mx_swiglu(x, acc[f + NF][i][g4 * 4 + q]);
+              if constexpr (OUT_F32) mx_store4(rb, nb, v, __float_as_uint(x));
+              else mx_store2(rb, nb, v, __builtin_bit_cast(uint16_t, (__bf16)x));
+            }
+          }
+        }
+      }
+    } else {
+      // lane = token l32 of a fragment; registers: columns 16 h + r
+      const int qld = ncols / 2, qsld = (int)((ncols / kMxBlock + 3) / 4 * 4);
+      void *qc = mx_uniform_ptr(g.q_codes + row_w * qld), *qs = mx_uniform_ptr(g.q_scales + row_w * qsld);
+      const uint32_t qcb = (uint32_t)(rows * qld), qsb = (uint32_t)(rows * qsld);
+      void *cu = mx_uniform_ptr(cb);
+      const uint32_t cub = g.C ? (uint32_t)(rows * ldc * ESZ) : 0u;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int rw = i * 32 + l32;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          float x[16];
+          uint32_t m = 0;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            x[r] = mx_swiglu(acc[f][i][r], acc[f + NF][i][r]);
+            m = max(m, __float_as_uint(x[r]) & 0x7FFFFFFFu);
+          }
+          const auto sm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+          const uint32_t byte = mx_scale_byte(max(sm[0], sm[1]), g.ceil_rule);
+          const float s = mx_scale_value(byte);
+          uint32_t c[2] = {0, 0};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            c[q] = mx_pack_f32<0>(c[q], x[8 * q], x[8 * q + 1], s);
+            c[q] = mx_pack_f32<1>(c[q], x[8 * q + 2], x[8 * q + 3], s);
+            c[q] = mx_pack_f32<2>(c[q], x[8 * q + 4], x[8 * q + 5], s);
+            c[q] = mx_pack_f32<3>(c[q], x[8 * q + 6], x[8 * q + 7], s);
+            if (byte == kMxNan) c[q] = 0;
+          }
+          const int col = col_w + f * 32;
+          const bool live = rw < rows && col < ncols;  // N is a whole number of blocks here
+          mx_store8(qc, qcb, live ? (uint32_t)(rw * qld + col / 2 + h * 8) : kNoStore, c[0], c[1]);
+          // blocks behind N up to the stride: zero padding (their columns are zeros)
+          mx_store1(qs, qsb, h == 0 && rw < rows && col / kMxBlock < qsld ? (uint32_t)(rw * qsld + col / kMxBlock)
+                                                                           : kNoStore, byte);
+          // 4-byte pieces: any row stride of C
+          const uint32_t v = live ? (uint32_t)(rw * ldc + col + h * 16) * ESZ : kNoStore;
+#pragma unroll
+          for (int q = 0; q < 4 * ESZ; ++q) {
+            if constexpr (OUT_F32) mx_store4(cu, cub, v + q * 4, __float_as_uint(x[q]));
+            else
+              mx_store4(cu, cub, v + q * 4,
+                        __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[2 * q], (__bf16)x[2 * q + 1]}));
+          }
+        }
+      }
+    }
+  };
+
+  // ---- products
+  MxJob cj{};
+  const auto multiply = [&](int step) MX_INLINE {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        if (TRANS) {
+          acc[i][j] = step == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                      wf[0][i], tf[0][j], acc[i][j], 4, 4, 0, (int)ws[0][i], 0, (int)ts[0][j])
+                                : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                      wf[1][i], tf[1][j], acc[i][j], 4, 4, 2, (int)ws[0][i], 2, (int)ts[0][j]);
+        } else {
+          acc[i][j] = step == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                      tf[0][j], wf[0][i], acc[i][j], 4, 4, 0, (int)ts[0][j], 0, (int)ws[0][i])
+                                : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                      tf[1][j], wf[1][i], acc[i][j], 4, 4, 2, (int)ts[0][j], 2, (int)ws[0][i]);
+        }
+      }
+    }
+  };
+  // stage st of the tile; refills its slot with stage p_st of the loading tile
+  const auto stage = [&](auto P, int st, int p_st, bool live) MX_INLINE {
+    constexpr int N = decltype(P)::value;
+    uint8_t *cur = N == 0 ? ring0 : N == 1 ? ring1 : N == 2 ? ring2 : ring3;
+    constexpr int M = (N + 1) % S;
+    const uint8_t *next = M == 0 ? ring0 : M == 1 ? ring1 : M == 2 ? ring2 : ring3;
+    read_codes(cur, 1, wf[1], tf[1]);
+    multiply(0);
+    // this stage is read; the next one must have landed for every wave.  The tile's first S
+    // stages have; behind them, S - 2 later stages' loads may be under way.
+    mx_wait_lds();
+    if (st + 1 >= S) mx_wait_vm<(S - 2) * Cfg::kDma>();
+    mx_barrier();
+    load_stage(cur, p_st, live);
+    read_scales(next, ws[1], ts[1]);
+    read_codes(next, 0, wf[0], tf[0]);
+    multiply(1);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) ws[0][i] = ws[1][i];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) ts[0][j] = ts[1][j];
+  };
+#pragma unroll 1
+  for (int64_t it = 0; tiles.has(it); ++it) {
+    cj = tiles.get(it);
+    clear();
+    if (cj.nst > 0) {
+      // the tile's first stages land: for this wave (behind them only the last tile's stores
+      // may be under way; TRANS stores adjacent pieces, which the compiler may merge), then for
+      // all
+      if (it > 0 && !TRANS) mx_wait_vm<(kStores < 63 ? kStores : 63)>();
+      else mx_wait_vm<0>();
+      mx_barrier();
+      read_scales(ring0, ws[0], ts[0]);
+      read_codes(ring0, 0, wf[0], tf[0]);
+      // stages that refill their slot from this tile, then those that fill it from the next
+      const int own = std::max(cj.nst - S, 0);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const int lo = part ? own : 0, hi = part ? cj.nst : own;
+        if (part) {
+          ++p_it;
+          p_find();
+        }
+#pragma unroll 1
+        for (int st = lo / S * S; st < hi; st += S) {
+          const auto one = [&](auto P) MX_INLINE {
+            constexpr int N = decltype(P)::value;
+            const int s = st + N;
+            if (N < S && s >= lo && s < hi) stage(P, s, part ? N : s + S, part == 0 || (p_live && N < pj.nst));
+          };
+          one(std::integral_constant<int, 0>{});
+          one(std::integral_constant<int, 1>{});
+          if constexpr (S > 2) one(std::integral_constant<int, 2>{});
+          if constexpr (S > 3) one(std::integral_constant<int, 3>{});
+        }
+      }
+      // a short tile did not use every slot
+      if (cj.nst < S) {
+        if (cj.nst <= 1) load_stage(ring1, 1, p_live && 1 < pj.nst);
+        if (S > 2 && cj.nst <= 2) load_stage(ring2, 2, p_live && 2 < pj.nst);
+        if (S > 3) load_stage(ring3, 3, p_live && 3 < pj.nst);
+      }
+    }
+    finish(cj);
+  }
+  mx_wait_vm<0>();  // loads into this workgroup's LDS end before it does
+}
+
+// persistent grid: whole multiples of the XCDs
+template <class Cfg, int GROUP, int EPI>
+hipError_t mx_launch(const MxGemmArgs &g, hipStream_t stream) {
+  constexpr int cols = EPI == NV4_EPI_SWIGLU ? Cfg::BN / 2 : Cfg::BN;
+  int64_t tiles;
+  if (GROUP == NV4_GROUP_M) {
+    if (g.M_cap == 0) return hipSuccess;
+    tiles = (g.M_cap / Cfg::BM + std::min<int64_t>(g.E, g.M_cap)) * ((g.N + cols - 1) / cols);
+  } else {
+    tiles = (int64_t)g.E * ((g.a_rows + Cfg::BM - 1) / Cfg::BM) * ((g.b_rows + Cfg::BN - 1) / Cfg::BN);
+    if (tiles == 0) return hipSuccess;
+  }
+  const int lds = Cfg::kStages * Cfg::kStageBytes + (kMxMaxExperts + 1) * 8;
+  const int per_cu = std::max(1, std::min(160 * 1024 / lds, Cfg::kWavesPerSimd * 4 / Cfg::NW));
+  const int64_t most = (int64_t)device_cu_count() * per_cu;
+  const unsigned grid = (unsigned)std::min<int64_t>((tiles + kMxXcds - 1) / kMxXcds * kMxXcds, most);
+  if constexpr (EPI == NV4_EPI_SWIGLU) {
+    if (g.q_codes) {
+      if (g.c_is_f32) k_mx_gemm<Cfg, GROUP, EPI, true, true><<<grid, Cfg::NT, 0, stream>>>(g);
+      else k_mx_gemm<Cfg, GROUP, EPI, false, true><<<grid, Cfg::NT, 0, stream>>>(g);
+      return hipGetLastError();
+    }
+  }
+  if (g.c_is_f32) k_mx_gemm<Cfg, GROUP, EPI, true, false><<<grid, Cfg::NT, 0, stream>>>(g);
+  else k_mx_gemm<Cfg, GROUP, EPI, false, false><<<grid, Cfg::NT, 0, stream>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace nv4

@@ -34,6 +34,7 @@ nvfp4     NVFP4 two-level block quantisation (rows and columns) and dequant.
 moe       routing, permutation, grouped GEMMs, SwiGLU and the weighted combine.
 pipeline  the whole expert-layer forward and backward with the GPU's storage
           roundings mirrored (for end-to-end reporting).
+mxfp4     MXFP4 block quantisation (32 elements, power-of-two scales) and its layer.
 philox    the Philox4x64-10 counter-based generator (stochastic rounding).
 
 Parity status: every function is pinned by tests under ``tests/`` against
@@ -48,4 +49,4 @@ FP4 rounding boundary, so the GPU tests compare stage by stage, each stage fed t
 GPU's own inputs, and gate the whole layer only loosely.
 """
 
-from . import formats, philox, nvfp4, moe, pipeline  # noqa: F401
+from . import formats, philox, nvfp4, moe, mxfp4, pipeline  # noqa: F401
