@@ -171,7 +171,10 @@ nv4_status mxfp4_grouped_gemm(const nv4_mx_tensor *A, const nv4_mx_tensor *B, co
     return fail(NV4_EINVAL, "%s: each operand must stay below 4 GiB of codes", fn);
   const int64_t ncols = group_mode == NV4_GROUP_K ? B->rows : N;
   if (C && ldc < ncols) return fail(NV4_EINVAL, "%s: ldc < columns of C", fn);
-  if (ncols >= kMost32 || (C && ldc > (1ll << 22))) return fail(NV4_EINVAL, "%s: too many columns", fn);
+  // columns and tiles are counted in 32 bits, a tile's rows of C addressed with 32-bit offsets
+  if (ncols > (1ll << 22) || (C && ldc > (1ll << 22))) return fail(NV4_EINVAL, "%s: too many columns", fn);
+  if ((group_mode == NV4_GROUP_K ? (int64_t)E * A->rows : M_cap) * ncols > (1ll << 40))
+    return fail(NV4_EINVAL, "%s: C is too large", fn);
   if (group_mode == NV4_GROUP_M) {
     const int64_t Nb = epilogue == NV4_EPI_SWIGLU ? 2 * N : N;
     if (N <= 0) return fail(NV4_EINVAL, "%s: N must be positive", fn);
@@ -246,7 +249,9 @@ nv4_status mx_moe_few(const void *x, nv4_dtype xtype, int64_t ldx, const float *
   if (otype != NV4_BF16 && otype != NV4_F32) return fail(NV4_EINVAL, "%s: bad output dtype", fn);
   if (H <= 0 || I <= 0) return fail(NV4_EINVAL, "%s: H and I must be positive", fn);
   if (H % 32 || I % 32) return fail(NV4_EALIGN, "%s: H and I must be multiples of 32", fn);
-  if (H > (1 << 20) || I > (1 << 20)) return fail(NV4_EINVAL, "%s: H or I too large", fn);
+  // byte offsets into an expert's matrix are 32-bit
+  if (H > (1 << 20) || I > (1 << 20) || I * H > 0xFFFFFF00ll)
+    return fail(NV4_EINVAL, "%s: H or I too large", fn);
   nv4_status st = check_tensor(fn, "w13", w13);
   if (st == NV4_OK) st = check_tensor(fn, "w2", w2);
   if (st != NV4_OK) return st;

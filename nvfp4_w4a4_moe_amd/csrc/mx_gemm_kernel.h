@@ -13,17 +13,16 @@
 // one token, and weight row n of a 32-row fragment sits at the operand row that makes them
 // consecutive (frag_row), so that an MX block is two lanes' registers.
 //
-// Data flow: HBM / L2 -> LDS by 16-byte DMA (stages of K = 128: 64 bytes of codes and 4 scale
-// bytes per row, a ring of kStages) -> registers (16-byte LDS reads, one per lane and
-// 64 K) -> MFMA.  In LDS, chunk q of row r sits at q ^ ((r >> 2) & 3): the 16 rows of one read
-// pass then cover all 64 banks.
+// Data flow: HBM / L2 -> LDS by 16-byte DMA (stages of K = 128 or 256: 64 or 128 bytes of codes
+// and 4 or 8 scale bytes per row, a ring of kStages) -> registers (16-byte LDS reads, one per
+// lane and 64 K) -> MFMA.
 //
-// Pipeline.  Stage s of a tile lives in ring slot s mod kStages.  A stage is two K = 64 steps;
-// in the middle of a stage every wave waits for its own loads of the next one, the workgroup
-// meets, and the slot just read is refilled: with this tile's stage s + kStages, or, in the
+// Pipeline.  Stage s of a tile lives in ring slot s mod kStages.  A stage is two or four K = 64
+// steps; before its last step every wave waits for its own loads of the next stage, the
+// workgroup meets, and the slot just read is refilled: with this tile's stage s + kStages, or, in the
 // tile's last kStages stages, with the next tile's stage of that slot, so that loads run
-// across tile ends and under the epilogue.  The next stage's first step is read while this
-// stage's second one multiplies.  Every stage issues the same number of loads (a load with
+// across tile ends and under the epilogue.  A step's operands are read while the step before
+// multiplies, each weight fragment into the registers that the one just used leaves.  Every stage issues the same number of loads (a load with
 // nothing to fetch has an offset behind the buffer) and every epilogue the same number of
 // branch-free stores, so a wait counts exactly what may still be under way.
 #pragma once
@@ -46,21 +45,46 @@ constexpr int kMxMaxExperts = 1024;
 constexpr int kMxXcds = 8;
 constexpr uint32_t kNoRow = 0xFFFFFF00u;  // a byte offset behind every buffer: loads return zeros
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES, int WAVES_PER_SIMD>
+// WAVES_M x WAVES_N waves of FM x FN 32 x 32 fragments; a ring of STAGES stages of STEPS K = 64
+// steps each
+template <int WAVES_M, int WAVES_N, int FM, int FN, int STEPS, int STAGES, int WAVES_PER_SIMD>
 struct MxTile {
   static constexpr int kWavesM = WAVES_M, kWavesN = WAVES_N, kFM = FM, kFN = FN;
-  static constexpr int kStages = STAGES, kWavesPerSimd = WAVES_PER_SIMD;
+  static constexpr int kSteps = STEPS, kStages = STAGES, kWavesPerSimd = WAVES_PER_SIMD;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int BM = WAVES_M * FM * 32;  // rows of A (tokens)
   static constexpr int BN = WAVES_N * FN * 32;  // rows of B (weights)
-  static constexpr int kCodes = (BM + BN) * 64, kStageBytes = kCodes + (BM + BN) * 4;
-  static constexpr int kCodeBlocks = (BM + BN) / 16;           // 1 KB DMAs: 16 rows
-  static constexpr int kCodeDma = (kCodeBlocks + NW - 1) / NW;  // per wave; surplus ones repeat the last block
-  static constexpr int kScaleBlocks = (BM + BN + 63) / 64;     // 256-byte DMAs: 64 rows
+  static constexpr int BK = STEPS * 64;
+  static constexpr int kRow = STEPS * 32;        // code bytes of a row per stage
+  static constexpr int kChunks = STEPS * 2;      // 16-byte chunks of them: one block each
+  static constexpr int kDwords = STEPS / 2;      // scale dwords of a row per stage
+  static constexpr int kCodes = (BM + BN) * kRow;
+  static constexpr int kCodeRows = 1024 / kRow;  // rows of one code DMA (64 lanes x 16 bytes)
+  static constexpr int kCodeBlocks = (BM + BN) / kCodeRows;
+  static constexpr int kCodeDma = (kCodeBlocks + NW - 1) / NW;  // per wave; surplus ones load rows behind the tile
+  static constexpr int kScaleRows = 64 / kDwords;  // rows of one scale DMA (64 lanes x 4 bytes)
+  static constexpr int kScaleBlocks = (BM + BN + kScaleRows - 1) / kScaleRows;
   static constexpr int kScaleDma = (kScaleBlocks + NW - 1) / NW;
   static constexpr int kDma = kCodeDma + kScaleDma;  // the same for every wave
-  static_assert((BM + BN) % 64 == 0, "whole scale blocks");
+  // (room for the surplus DMAs of either kind)
+  static constexpr int kScaleBase = NW * kCodeDma * 1024;
+  static constexpr int kStageBytes = kScaleBase + NW * kScaleDma * 256;
+  // tile rows whose codes, and whose scales, one wave loads: a lane looks one of each up
+  static constexpr int kWaveCodeRows = kCodeDma * kCodeRows, kWaveScaleRows = kScaleDma * kScaleRows;
+  static_assert(kWaveCodeRows <= 64 && kWaveScaleRows <= 64, "a lane for each row");
+  static constexpr bool kSameRows = kWaveCodeRows == kWaveScaleRows;
+  // every wave loads rows of one operand only
+  static constexpr bool kOneSide = kSameRows && BN % kWaveCodeRows == 0 && BM % kWaveCodeRows == 0;
+  static_assert(STEPS == 2 || STEPS == 4, "stages of K = 128 or 256");
+  static_assert(BN % 64 == 0 && (BM + BN) % kCodeRows == 0, "DMA blocks of one operand");
 };
+
+// Ring position of chunk q of tile row r: the 16 rows of one LDS read pass cover all 64 banks
+// (rows of 64 bytes: 4 to a bank sweep; of 128: 2).
+template <class Cfg>
+__device__ __forceinline__ int mx_swz(int q, int r) {
+  return Cfg::kSteps == 2 ? q ^ ((r >> 2) & 3) : q ^ ((r >> 1) & 7);
+}
 
 typedef __attribute__((address_space(3))) void *mx_lds_ptr;
 __device__ __forceinline__ void mx_dma16(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
@@ -150,6 +174,9 @@ __device__ __forceinline__ int mx_table(const int *p) {
 // lane half h holds operand row 8 (r / 4) + 4 h + r % 4; it shall be column 16 h + r.
 __device__ __forceinline__ int frag_row(int i) { return ((i >> 2) & 1) * 16 + (i >> 3) * 4 + (i & 3); }
 
+// four code dwords as the instruction's operand (FP4 reads the first four of eight)
+__device__ __forceinline__ i32x8 mx_operand(int4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+
 // gate / (1 + exp(-gate)) * up in FP32 (hardware exp2 and reciprocal, relative error ~1e-7)
 __device__ __forceinline__ float mx_swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
@@ -157,65 +184,69 @@ __device__ __forceinline__ float mx_swiglu(float g, float u) {
 
 struct MxJob {
   int e, nt;
-  int64_t m0, m_end;   // rows of A / C
-  int64_t k_lo, k_hi;  // contraction range
-  int nst;             // stages
+  int m0, m_end;   // rows of A / C
+  int k_lo, nst;   // contraction: start and stages
+  int k_len;
 };
 
+// The workgroup's sequence of tiles.  GROUP_M: logical tiles in XCD order (workgroup i runs on
+// XCD i % 8): the workgroups of one XCD take consecutive tiles, which share A rows and an
+// expert's weights in its L2.  GROUP_K: experts by decreasing length and the tiles dealt out in
+// turn, forwards then backwards, so that every workgroup gets long and short ones; the empty
+// ones come last.
+// Finding a tile takes a search, so a wave finds 64 at a time, one per lane, and each is then a
+// few lane reads away.
 template <class Cfg, int GROUP, int EPI>
 struct MxTiles {
-  // The workgroup's sequence of tiles.  GROUP_M: logical tiles in XCD order (workgroup i runs
-  // on XCD i % 8): the workgroups of one XCD take consecutive tiles, which share A rows and
-  // an expert's weights in its L2.  GROUP_K: experts by decreasing length and the tiles dealt
-  // out in turn, forwards then backwards, so that every workgroup gets long and short ones.
   const MxGemmArgs &g;
   const int *off;  // the expert offsets
   const int *tab;  // GROUP_M: first M tile of each expert; GROUP_K: experts by length
-  int64_t total;
+  int total;
   int ntn;
-  __device__ int64_t index(int64_t it) const {  // grows with it
-    const int64_t G = gridDim.x;
-    if (GROUP == NV4_GROUP_K) return it * G + ((it & 1) ? G - 1 - blockIdx.x : blockIdx.x);
-    const int64_t per = G / kMxXcds;
-    const int64_t slot = blockIdx.x < per * kMxXcds ? (blockIdx.x % kMxXcds) * per + blockIdx.x / kMxXcds : blockIdx.x;
-    return it * G + slot;
+  int en, m, lo, hi;  // this lane's tile: expert | column tile << 10, first row, and row end or K range
+  __device__ __forceinline__ int index(int it) const {  // grows with it
+    const int G = gridDim.x, b = blockIdx.x;
+    if (GROUP == NV4_GROUP_K) return it * G + ((it & 1) ? G - 1 - b : b);
+    const int per = G / kMxXcds;
+    return it * G + (b < per * kMxXcds ? (b % kMxXcds) * per + b / kMxXcds : b);
   }
-  __device__ bool has(int64_t it) const { return index(it) < total; }
-  __device__ MxJob get(int64_t it) const {
-    MxJob j;
-    const int64_t L = index(it);
+  __device__ __forceinline__ bool has(int it) const { return index(it) < total; }
+  __device__ __forceinline__ void find(int it) {
+    const int L = index(it + (int)(threadIdx.x & 63));
+    en = m = lo = hi = 0;
+    if (L >= total) return;
     if (GROUP == NV4_GROUP_M) {
-      const int mt = (int)(L / ntn);
-      j.nt = (int)(L - (int64_t)mt * ntn);
-      // last expert with tab[e] <= mt (it owns at least one tile); tab does not decrease
-      int n = 0;
-      for (int e = 0; e < g.E; e += 64) {
-        const int i = e + (threadIdx.x & 63);
-        n += __popcll(__ballot(i < g.E && mx_table(tab + min(i, g.E)) <= mt));
+      const int mt = L / ntn;
+      int e = 0, top = g.E - 1;  // last expert with tab[e] <= mt (it owns at least one tile)
+      while (e < top) {
+        const int mid = (e + top + 1) >> 1;
+        if (tab[mid] <= mt) e = mid; else top = mid - 1;
       }
-      j.e = n - 1;
-      j.m0 = (int64_t)mx_table(off + j.e) + (int64_t)(mt - mx_table(tab + j.e)) * Cfg::BM;
-      j.m_end = std::min<int64_t>(mx_table(off + j.e + 1), g.M_cap);
-      j.k_lo = 0;
-      j.k_hi = g.K;
+      en = e | (L - mt * ntn) << 10;
+      m = off[e] + (mt - tab[e]) * Cfg::BM;
+      hi = min(off[e + 1], (int)g.M_cap);
     } else {
-      const int tn = (int)((g.a_rows + Cfg::BM - 1) / Cfg::BM);
-      const int per_e = tn * ntn;
-      const int rank = (int)(L / per_e), r = (int)(L - (int64_t)rank * per_e);
-      j.e = mx_table(tab + rank);
-      j.nt = r % ntn;
-      j.m0 = (int64_t)(r / ntn) * Cfg::BM;
-      j.m_end = g.a_rows;
-      j.k_lo = std::min<int64_t>(mx_table(off + j.e), g.K);
-      j.k_hi = std::max<int64_t>(std::min<int64_t>(mx_table(off + j.e + 1), g.K), j.k_lo);
+      const int tn = (int)((g.a_rows + Cfg::BM - 1) / Cfg::BM), per_e = tn * ntn;
+      const int rank = L / per_e, r = L - rank * per_e, e = tab[rank];
+      en = e | (r % ntn) << 10;
+      m = r / ntn * Cfg::BM;
+      lo = min(off[e], (int)g.K);
+      hi = max(min(off[e + 1], (int)g.K), lo);
     }
-    j.e = __builtin_amdgcn_readfirstlane(j.e);
-    j.nt = __builtin_amdgcn_readfirstlane(j.nt);
-    j.m0 = mx_uniform(j.m0);
-    j.m_end = mx_uniform(j.m_end);
-    j.k_lo = mx_uniform(j.k_lo);
-    j.k_hi = mx_uniform(j.k_hi);
-    j.nst = (int)((j.k_hi - j.k_lo + 127) / 128);
+  }
+  // tile `it`, called with it = 0, 1, 2, ..
+  __device__ __forceinline__ MxJob get(int it) {
+    const int l = it & 63;
+    if (l == 0) find(it);
+    const int x = __builtin_amdgcn_readlane(en, l), h = __builtin_amdgcn_readlane(hi, l);
+    MxJob j;
+    j.e = x & 1023;
+    j.nt = x >> 10;
+    j.m0 = __builtin_amdgcn_readlane(m, l);
+    j.m_end = GROUP == NV4_GROUP_M ? h : (int)g.a_rows;
+    j.k_lo = GROUP == NV4_GROUP_M ? 0 : __builtin_amdgcn_readlane(lo, l);
+    j.k_len = GROUP == NV4_GROUP_M ? (int)g.K : h - j.k_lo;
+    j.nst = (j.k_len + Cfg::BK - 1) / Cfg::BK;
     return j;
   }
 };
@@ -254,6 +285,7 @@ void k_mx_gemm(MxGemmArgs g) {
   static_assert(S >= 2 && S <= 4, "ring of 2 to 4 slots");
   __shared__ int tab[kMxMaxExperts + 1];
   __shared__ int off[kMxMaxExperts + 1];
+  __shared__ int rows_c[Cfg::NW][64], rows_s[Cfg::kSameRows ? 1 : Cfg::NW][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Cfg::kWavesN, wn = wave % Cfg::kWavesN;
@@ -265,7 +297,7 @@ void k_mx_gemm(MxGemmArgs g) {
   // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty)
   for (int e = tid; e <= g.E; e += NT) off[e] = std::max(g.offsets[e], 0);
   __syncthreads();
-  MxTiles<Cfg, GROUP, EPI> tiles{g, off, tab, 0, 0};
+  MxTiles<Cfg, GROUP, EPI> tiles{g, off, tab, 0, 0, 0, 0, 0, 0};
   if (GROUP == NV4_GROUP_M) {
     int *scratch = reinterpret_cast<int *>(ring0);
     const int per = (g.E + NT - 1) / NT;
@@ -294,7 +326,7 @@ void k_mx_gemm(MxGemmArgs g) {
     __syncthreads();
     constexpr int cols = SWIGLU ? BN / 2 : BN;
     tiles.ntn = (int)((g.N + cols - 1) / cols);
-    tiles.total = mx_uniform((int64_t)tab[g.E] * tiles.ntn);
+    tiles.total = __builtin_amdgcn_readfirstlane(tab[g.E] * tiles.ntn);
   } else {
     for (int e = tid; e < g.E; e += NT) {
       const int n = off[e + 1] - off[e];
@@ -307,113 +339,119 @@ void k_mx_gemm(MxGemmArgs g) {
     }
     __syncthreads();
     tiles.ntn = (int)((g.b_rows + BN - 1) / BN);
-    tiles.total = (int64_t)g.E * ((g.a_rows + BM - 1) / BM) * tiles.ntn;
+    tiles.total = (int)(g.E * ((g.a_rows + BM - 1) / BM) * tiles.ntn);
   }
 
   // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included)
   uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
-  const int qrow = lane >> 2, qpos = lane & 3;
-  int64_t p_it = 0;  // the loading tile
-  MxJob pj{};
-  bool p_live;  // there is one
+  const int qrow = lane / Cfg::kChunks, qpos = lane % Cfg::kChunks;    // row and ring position in a code DMA
+  const int srow = lane / Cfg::kDwords, sdw = lane % Cfg::kDwords;     // row and dword in a scale DMA
+  MxJob cj{};   // the tile being multiplied
+  MxJob pj{};   // the loading tile: the same, and the next one towards its end
+  bool p_live;  // there is one with at least one stage
+  const bool gather = GROUP == NV4_GROUP_M && g.a_rows_index != nullptr;
+  // Row indices of a tile come through LDS as well: each wave loads its lanes' own (a row of B
+  // or none has the offset behind the buffer) well before they are needed.
+  const auto load_index = [&](const MxJob &j) MX_INLINE {
+    const auto one = [&](int r, int *dst) MX_INLINE {
+      const int row = j.m0 + (r - BN);
+      mx_dma4(g.a_rows_index, (uint32_t)g.M_cap * 4u, reinterpret_cast<uint8_t *>(dst),
+              r >= BN && r < BN + BM && row < j.m_end ? (uint32_t)row * 4u : kNoRow);
+    };
+    one(wave * Cfg::kWaveCodeRows + lane, rows_c[wave]);
+    if constexpr (!Cfg::kSameRows) one(wave * Cfg::kWaveScaleRows + lane, rows_s[wave]);
+  };
+  // operand row of tile row r, or -1; idx: what load_index brought
+  const auto p_row = [&](int r, const int *idx) MX_INLINE -> int {
+    int row = pj.m0 + (r - BN);
+    row = r < BN + BM && row < pj.m_end ? row : -1;
+    if (gather && row >= 0) row = min(max(mx_table(idx + lane), 0), (int)g.a_rows - 1);
+    if (Cfg::kOneSide ? wave * Cfg::kWaveCodeRows < BN : r < BN) row = (int)mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
+    return row;
+  };
   const auto p_setup = [&]() MX_INLINE {
+    const int mc = p_row(wave * Cfg::kWaveCodeRows + lane, rows_c[wave]);
+    const int ms = Cfg::kSameRows ? mc : p_row(wave * Cfg::kWaveScaleRows + lane, rows_s[wave]);
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
-      const int b = std::min(wave * Cfg::kCodeDma + i, Cfg::kCodeBlocks - 1);
-      const int r = b * 16 + qrow;
-      int64_t row;
-      if (r < BN) {
-        row = mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
-      } else {
-        row = pj.m0 + (r - BN);
-        if (row >= pj.m_end) row = -1;
-        else if (GROUP == NV4_GROUP_M && g.a_rows_index) row = min((int64_t)max(g.a_rows_index[row], 0), g.a_rows - 1);
-      }
-      off_c[i] = row < 0 ? kNoRow : (uint32_t)(row * ld) + (uint32_t)((qpos ^ ((r >> 2) & 3)) * 16);
+      const int in = i * Cfg::kCodeRows + qrow, row = __shfl(mc, in, 64);
+      off_c[i] = row < 0 ? kNoRow
+                         : (uint32_t)row * (uint32_t)ld +
+                               (uint32_t)(mx_swz<Cfg>(qpos, wave * Cfg::kWaveCodeRows + in) * 16);
     }
 #pragma unroll
     for (int i = 0; i < Cfg::kScaleDma; ++i) {
-      const int b = std::min(wave * Cfg::kScaleDma + i, Cfg::kScaleBlocks - 1);
-      const int r = b * 64 + lane;
-      int64_t row;
-      if (r < BN) {
-        row = mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
-      } else {
-        row = pj.m0 + (r - BN);
-        if (row >= pj.m_end) row = -1;
-        else if (GROUP == NV4_GROUP_M && g.a_rows_index) row = min((int64_t)max(g.a_rows_index[row], 0), g.a_rows - 1);
-      }
-      off_s[i] = row < 0 ? kNoRow : (uint32_t)(row * sld);
+      const int row = __shfl(ms, i * Cfg::kScaleRows + srow, 64);
+      off_s[i] = row < 0 ? kNoRow : (uint32_t)row * (uint32_t)sld + (uint32_t)(sdw * 4);
     }
   };
-  // loading tile: the first one from p_it on with at least one stage (GROUP_K: an empty
-  // range has none)
-  const auto p_find = [&]() MX_INLINE {
-    p_live = false;
-    while (tiles.has(p_it)) {
-      pj = tiles.get(p_it);
-      if (pj.nst > 0) {
-        p_live = true;
-        p_setup();
-        break;
-      }
-      ++p_it;
-    }
+  // the loading tile becomes tile `it`, if there is one
+  const auto p_next = [&](int it) MX_INLINE {
+    p_live = tiles.has(it);
+    if (p_live) pj = tiles.get(it);
+    p_live = p_live && pj.nst > 0;
   };
   // one stage of the loading tile into a ring slot (live: there is such a stage)
-  const auto load_stage = [&](uint8_t *dst, int p_st, bool live) MX_INLINE {
-    const uint32_t kc = (uint32_t)((pj.k_lo + (int64_t)p_st * 128) / 2), ks = kc / 16;
-    // elements of this stage (may exceed 128)
-    const int left = live ? (int)((pj.k_hi - pj.k_lo) - (int64_t)p_st * 128) : 0;
+  const auto load_stage = [&](uint8_t *dst, int p_st, bool live, bool of_next) MX_INLINE {
+    const int k_lo = of_next ? pj.k_lo : cj.k_lo, k_len = of_next ? pj.k_len : cj.k_len;
+    const uint32_t kc = (uint32_t)(k_lo + p_st * Cfg::BK) / 2, ks = kc / 16;
+    const int left = live ? k_len - p_st * Cfg::BK : 0;  // elements of this stage (may exceed BK)
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
-      const int b = std::min(wave * Cfg::kCodeDma + i, Cfg::kCodeBlocks - 1);
-      const bool in_k = (int)((qpos ^ (((b * 16 + qrow) >> 2) & 3)) * 32) < left;
-      const uint32_t v = (off_c[i] == kNoRow || !in_k) ? kNoRow : off_c[i] + kc;
-      const bool isb = b * 16 < BN;
+      const int b = wave * Cfg::kCodeDma + i;
+      const bool in_k = mx_swz<Cfg>(qpos, b * Cfg::kCodeRows + qrow) * 32 < left;
+      // (saturating: without a row the sum stays behind the buffer)
+      const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], kc) : kNoRow;
+      const bool isb = b * Cfg::kCodeRows < BN;
       mx_dma16(isb ? g.b_codes : g.a_codes, isb ? b_bytes : a_bytes, dst + b * 1024, v);
     }
 #pragma unroll
     for (int i = 0; i < Cfg::kScaleDma; ++i) {
-      const int b = std::min(wave * Cfg::kScaleDma + i, Cfg::kScaleBlocks - 1);
-      const uint32_t v = (off_s[i] == kNoRow || left <= 0) ? kNoRow : off_s[i] + ks;
-      const bool isb = b * 64 < BN;
-      mx_dma4(isb ? g.b_scales : g.a_scales, isb ? b_sbytes : a_sbytes, dst + Cfg::kCodes + b * 256, v);
+      const int b = wave * Cfg::kScaleDma + i;
+      const uint32_t v = sdw * 128 < left ? __builtin_elementwise_add_sat(off_s[i], ks) : kNoRow;
+      const bool isb = b * Cfg::kScaleRows < BN;
+      mx_dma4(isb ? g.b_scales : g.a_scales, isb ? b_sbytes : a_sbytes, dst + Cfg::kScaleBase + b * 256, v);
     }
   };
-  static_assert(BN % 64 == 0, "scale blocks of one operand");
 
-  p_find();
-  load_stage(ring0, 0, p_live);
-  load_stage(ring1, 1, p_live);
-  if constexpr (S > 2) load_stage(ring2, 2, p_live);
-  if constexpr (S > 3) load_stage(ring3, 3, p_live);
+  p_next(0);
+  if (gather) {
+    load_index(pj);
+    mx_wait_vm<0>();
+  }
+  p_setup();
+  load_stage(ring0, 0, p_live && 0 < pj.nst, true);
+  load_stage(ring1, 1, p_live && 1 < pj.nst, true);
+  if constexpr (S > 2) load_stage(ring2, 2, p_live && 2 < pj.nst, true);
+  if constexpr (S > 3) load_stage(ring3, 3, p_live && 3 < pj.nst, true);
 
-  // ---- fragments of one K = 64 step: chunk 2 step + h of the wave's rows
-  i32x8 wf[2][FN], tf[2][FM];
-  uint32_t ws[2][FN] = {}, ts[2][FM] = {};  // scale dwords shifted so that byte 0 is step 0's, byte 2 step 1's
+  // ---- fragments of one K = 64 step.  Lane half h takes the chunks h KS .. h KS + KS - 1 of a
+  // stage's rows, one per step: their scale bytes are then bytes 0 .. KS - 1 of what one LDS
+  // read of the lane gives (K is permuted alike for both operands).
+  constexpr int KS = Cfg::kSteps;
+  int4 wf[FN], tf[2][FM];
+  uint32_t ws[FN] = {}, ts[FM] = {};
   const int w_row = wn * FN * 32 + l32, t_row = BN + wm * FM * 32 + l32;
-  const int sw = (l32 >> 2) & 3;  // the same for every fragment (rows differ by multiples of 32)
-  const auto read_codes = [&](const uint8_t *st, int step, i32x8 (&w)[FN], i32x8 (&t)[FM]) {
-    const int pos = ((2 * step + h) ^ sw) * 16;
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      const int4 v = *reinterpret_cast<const int4 *>(st + (w_row + f * 32) * 64 + pos);
-      w[f] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-    }
+  const auto chunk = [&](const uint8_t *st, int row, int step) MX_INLINE {
+    // (rows of different fragments differ by multiples of 32: one swizzle)
+    return *reinterpret_cast<const int4 *>(st + row * Cfg::kRow + mx_swz<Cfg>(h * KS + step, l32) * 16);
+  };
+  const auto scale = [&](const uint8_t *st, int row) MX_INLINE -> uint32_t {
+    const uint8_t *p = st + Cfg::kScaleBase + row * (Cfg::kDwords * 4) + h * KS;
+    if constexpr (KS == 4) return *reinterpret_cast<const uint32_t *>(p);
+    else return *reinterpret_cast<const uint16_t *>(p);
+  };
+  const auto read_first = [&](const uint8_t *st) MX_INLINE {
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
-      const int4 v = *reinterpret_cast<const int4 *>(st + (t_row + f * 32) * 64 + pos);
-      t[f] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      tf[0][f] = chunk(st, t_row + f * 32, 0);
+      ts[f] = scale(st, t_row + f * 32);
     }
-  };
-  const auto read_scales = [&](const uint8_t *st, uint32_t (&w)[FN], uint32_t (&t)[FM]) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
-      w[f] = *reinterpret_cast<const uint32_t *>(st + Cfg::kCodes + (w_row + f * 32) * 4) >> (8 * h);
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-      t[f] = *reinterpret_cast<const uint32_t *>(st + Cfg::kCodes + (t_row + f * 32) * 4) >> (8 * h);
+    for (int f = 0; f < FN; ++f) {
+      wf[f] = chunk(st, w_row + f * 32, 0);
+      ws[f] = scale(st, w_row + f * 32);
+    }
   };
 
   f32x16 acc[FN][FM];
@@ -433,30 +471,35 @@ void k_mx_gemm(MxGemmArgs g) {
   const auto finish = [&](const MxJob &j) MX_INLINE {
     const int ncols = (int)(GROUP == NV4_GROUP_K ? g.b_rows : g.N);
     const int col_w = j.nt * (SWIGLU ? BN / 2 : BN) + wn * NF * 32;  // this wave's first column
-    const int64_t row_w = j.m0 + wm * FM * 32;
+    const int64_t row_w = (int64_t)j.m0 + wm * FM * 32;
     const int rows = (int)std::min<int64_t>(std::max<int64_t>(j.m_end - row_w, 0), FM * 32);
     const int ldc = (int)g.ldc;
     char *cb = static_cast<char *>(g.C) + ((GROUP == NV4_GROUP_K ? (int64_t)j.e * g.a_rows : 0) + row_w) * g.ldc * ESZ;
     if constexpr (!TRANS) {
       // lane = column l32 of a fragment; registers: rows 8 (r / 4) + 4 h + r % 4
+      uint32_t voff[NF];
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const int col = col_w + f * 32 + l32;
+        voff[f] = col < ncols ? (uint32_t)((h * 4 * ldc + col) * ESZ) : kNoStore;
+      }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
-          // the group's 8 rows: a store behind the valid ones falls behind the buffer
-          const int r0 = i * 32 + g4 * 8;
-          const uint32_t nb = (uint32_t)(std::min(std::max(rows - r0, 0), 8) * ldc * ESZ);
-          void *rb = mx_uniform_ptr(cb + (int64_t)r0 * ldc * ESZ);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            // rows r0 (lane half 0) and r0 + 4: a store behind the valid rows falls behind the
+            // buffer
+            const int r0 = i * 32 + g4 * 8 + q;
+            const uint32_t nb = r0 + 4 < rows ? (uint32_t)(5 * ldc * ESZ) : r0 < rows ? (uint32_t)(ldc * ESZ) : 0u;
+            void *rb = mx_uniform_ptr(cb + (int64_t)r0 * ldc * ESZ);
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-              const int col = col_w + f * 32 + l32;
-              const uint32_t v = col < ncols ? (uint32_t)(((q + h * 4) * ldc + col) * ESZ) : kNoStore;
               float x = acc[f][i][g4 * 4 + q];
               if constexpr (SWIGLU) x = mx_swiglu(x, acc[f + NF][i][g4 * 4 + q]);
-              if constexpr (OUT_F32) mx_store4(rb, nb, v, __float_as_uint(x));
-              else mx_store2(rb, nb, v, __builtin_bit_cast(uint16_t, (__bf16)x));
+              if constexpr (OUT_F32) mx_store4(rb, nb, voff[f], __float_as_uint(x));
+              else mx_store2(rb, nb, voff[f], __builtin_bit_cast(uint16_t, (__bf16)x));
             }
           }
         }
@@ -495,9 +538,11 @@ void k_mx_gemm(MxGemmArgs g) {
           const int col = col_w + f * 32;
           const bool live = rw < rows && col < ncols;  // N is a whole number of blocks here
           mx_store8(qc, qcb, live ? (uint32_t)(rw * qld + col / 2 + h * 8) : kNoStore, c[0], c[1]);
-          // blocks behind N up to the stride: zero padding (their columns are zeros)
-          mx_store1(qs, qsb, h == 0 && rw < rows && col / kMxBlock < qsld ? (uint32_t)(rw * qsld + col / kMxBlock)
-                                                                           : kNoStore, byte);
+          mx_store1(qs, qsb, h == 0 && live ? (uint32_t)(rw * qsld + col / kMxBlock) : kNoStore, byte);
+          if (col < ncols && col + kMxBlock >= ncols) {  // the last block: zeros up to the stride
+            for (int b = col / kMxBlock + 1; b < qsld; ++b)
+              mx_store1(qs, qsb, h == 0 && rw < rows ? (uint32_t)(rw * qsld + b) : kNoStore, 0u);
+          }
           // 4-byte pieces: any row stride of C
           const uint32_t v = live ? (uint32_t)(rw * ldc + col + h * 16) * ESZ : kNoStore;
 #pragma unroll
@@ -513,51 +558,80 @@ void k_mx_gemm(MxGemmArgs g) {
   };
 
   // ---- products
-  MxJob cj{};
-  const auto multiply = [&](int step) MX_INLINE {
+  // the products of weight fragment i in a step
+  const auto multiply = [&](auto STEP, int i) MX_INLINE {
+    constexpr int step = decltype(STEP)::value, p = step & 1;
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        if (TRANS) {
-          acc[i][j] = step == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                      wf[0][i], tf[0][j], acc[i][j], 4, 4, 0, (int)ws[0][i], 0, (int)ts[0][j])
-                                : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                      wf[1][i], tf[1][j], acc[i][j], 4, 4, 2, (int)ws[0][i], 2, (int)ts[0][j]);
-        } else {
-          acc[i][j] = step == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                      tf[0][j], wf[0][i], acc[i][j], 4, 4, 0, (int)ts[0][j], 0, (int)ws[0][i])
-                                : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                      tf[1][j], wf[1][i], acc[i][j], 4, 4, 2, (int)ts[0][j], 2, (int)ws[0][i]);
-        }
-      }
+    for (int j = 0; j < FM; ++j) {
+      if (TRANS)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            mx_operand(wf[i]), mx_operand(tf[p][j]), acc[i][j], 4, 4, step, (int)ws[i], step, (int)ts[j]);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            mx_operand(tf[p][j]), mx_operand(wf[i]), acc[i][j], 4, 4, step, (int)ts[j], step, (int)ws[i]);
     }
+    // Products stay where they are written.  (They touch no memory, so nothing else keeps the
+    // compiler from reading every step's fragments first, for which the registers do not last.)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
   // stage st of the tile; refills its slot with stage p_st of the loading tile
-  const auto stage = [&](auto P, int st, int p_st, bool live) MX_INLINE {
+  const auto stage = [&](auto P, int st, int p_st, bool live, bool of_next) MX_INLINE {
     constexpr int N = decltype(P)::value;
     uint8_t *cur = N == 0 ? ring0 : N == 1 ? ring1 : N == 2 ? ring2 : ring3;
     constexpr int M = (N + 1) % S;
     const uint8_t *next = M == 0 ? ring0 : M == 1 ? ring1 : M == 2 ? ring2 : ring3;
-    read_codes(cur, 1, wf[1], tf[1]);
-    multiply(0);
-    // this stage is read; the next one must have landed for every wave.  The tile's first S
-    // stages have; behind them, S - 2 later stages' loads may be under way.
+    const auto step = [&](auto STEP) MX_INLINE {
+      constexpr int s = decltype(STEP)::value;
+#pragma unroll
+      for (int f = 0; f < FM; ++f) tf[(s + 1) & 1][f] = chunk(cur, t_row + f * 32, s + 1);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        multiply(STEP, i);
+        wf[i] = chunk(cur, w_row + i * 32, s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    if constexpr (KS == 4) {
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
+    }
+    // The last step: half of its products, then the stage is read, and the next one must have
+    // landed for every wave.  The tile's first S stages have; behind them, S - 2 later stages'
+    // loads may be under way.
+    constexpr std::integral_constant<int, KS - 1> last{};
+    constexpr int half = (FN + 1) / 2;
+#pragma unroll
+    for (int i = 0; i < half; ++i) multiply(last, i);
     mx_wait_lds();
     if (st + 1 >= S) mx_wait_vm<(S - 2) * Cfg::kDma>();
     mx_barrier();
-    load_stage(cur, p_st, live);
-    read_scales(next, ws[1], ts[1]);
-    read_codes(next, 0, wf[0], tf[0]);
-    multiply(1);
+    load_stage(cur, p_st, live, of_next);
 #pragma unroll
-    for (int i = 0; i < FN; ++i) ws[0][i] = ws[1][i];
+    for (int f = 0; f < FM; ++f) tf[0][f] = chunk(next, t_row + f * 32, 0);
+    uint32_t nw[FN], nt[FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) ts[0][j] = ts[1][j];
+    for (int f = 0; f < FM; ++f) nt[f] = scale(next, t_row + f * 32);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) nw[f] = scale(next, w_row + f * 32);
+#pragma unroll
+    for (int i = 0; i < half; ++i) wf[i] = chunk(next, w_row + i * 32, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = half; i < FN; ++i) {
+      multiply(last, i);
+      wf[i] = chunk(next, w_row + i * 32, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) ts[f] = nt[f];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) ws[f] = nw[f];
   };
 #pragma unroll 1
-  for (int64_t it = 0; tiles.has(it); ++it) {
-    cj = tiles.get(it);
+  for (int it = 0; tiles.has(it); ++it) {
+    cj = pj;
     clear();
     if (cj.nst > 0) {
       // the tile's first stages land: for this wave (behind them only the last tile's stores
@@ -566,23 +640,27 @@ void k_mx_gemm(MxGemmArgs g) {
       if (it > 0 && !TRANS) mx_wait_vm<(kStores < 63 ? kStores : 63)>();
       else mx_wait_vm<0>();
       mx_barrier();
-      read_scales(ring0, ws[0], ts[0]);
-      read_codes(ring0, 0, wf[0], tf[0]);
+      p_next(it + 1);
+      if (gather && p_live) load_index(pj);
+      read_first(ring0);
       // stages that refill their slot from this tile, then those that fill it from the next
       const int own = std::max(cj.nst - S, 0);
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         const int lo = part ? own : 0, hi = part ? cj.nst : own;
-        if (part) {
-          ++p_it;
-          p_find();
+        if (part && p_live) {
+          if (gather) {  // behind the indices: the loads of `own` stages
+            if (own >= S - 1) mx_wait_vm<(S - 1) * Cfg::kDma>();
+            else mx_wait_vm<0>();
+          }
+          p_setup();
         }
 #pragma unroll 1
         for (int st = lo / S * S; st < hi; st += S) {
           const auto one = [&](auto P) MX_INLINE {
             constexpr int N = decltype(P)::value;
             const int s = st + N;
-            if (N < S && s >= lo && s < hi) stage(P, s, part ? N : s + S, part == 0 || (p_live && N < pj.nst));
+            if (N < S && s >= lo && s < hi) stage(P, s, part ? N : s + S, part == 0 || (p_live && N < pj.nst), part);
           };
           one(std::integral_constant<int, 0>{});
           one(std::integral_constant<int, 1>{});
@@ -592,10 +670,12 @@ void k_mx_gemm(MxGemmArgs g) {
       }
       // a short tile did not use every slot
       if (cj.nst < S) {
-        if (cj.nst <= 1) load_stage(ring1, 1, p_live && 1 < pj.nst);
-        if (S > 2 && cj.nst <= 2) load_stage(ring2, 2, p_live && 2 < pj.nst);
-        if (S > 3) load_stage(ring3, 3, p_live && 3 < pj.nst);
+        if (cj.nst <= 1) load_stage(ring1, 1, p_live && 1 < pj.nst, 1);
+        if (S > 2 && cj.nst <= 2) load_stage(ring2, 2, p_live && 2 < pj.nst, 1);
+        if (S > 3) load_stage(ring3, 3, p_live && 3 < pj.nst, 1);
       }
+    } else {
+      p_next(it + 1);
     }
     finish(cj);
   }
@@ -614,7 +694,7 @@ hipError_t mx_launch(const MxGemmArgs &g, hipStream_t stream) {
     tiles = (int64_t)g.E * ((g.a_rows + Cfg::BM - 1) / Cfg::BM) * ((g.b_rows + Cfg::BN - 1) / Cfg::BN);
     if (tiles == 0) return hipSuccess;
   }
-  const int lds = Cfg::kStages * Cfg::kStageBytes + (kMxMaxExperts + 1) * 8;
+  const int lds = Cfg::kStages * Cfg::kStageBytes + (kMxMaxExperts + 1) * 8 + Cfg::NW * 512;
   const int per_cu = std::max(1, std::min(160 * 1024 / lds, Cfg::kWavesPerSimd * 4 / Cfg::NW));
   const int64_t most = (int64_t)device_cu_count() * per_cu;
   const unsigned grid = (unsigned)std::min<int64_t>((tiles + kMxXcds - 1) / kMxXcds * kMxXcds, most);

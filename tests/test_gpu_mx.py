@@ -408,7 +408,8 @@ def few_case(gpu_lib, T, E, k, H, I, seed=0, rule=M.FLOOR):
 @pytest.mark.parametrize("T,E,k,H,I", [
     (1, 8, 2, 64, 32), (1, 2, 1, 32, 32), (2, 40, 3, 96, 160), (5, 16, 8, 160, 64), (16, 4, 2, 288, 96),
     (17, 3, 3, 128, 224), (33, 130, 6, 64, 64), (64, 8, 2, 544, 288), (64, 2, 2, 1056, 32), (7, 300, 32, 64, 32),
-    (64, 1, 1, 64, 64), (3, 1024, 4, 32, 32), (9, 520, 2, 2080, 32)])
+    (64, 1, 1, 64, 64), (3, 1024, 4, 32, 32), (9, 520, 2, 2080, 32),
+    (2, 8, 8, 64, 1056), (8, 2, 2, 64, 32), (4, 4, 4, 4128, 32), (3, 64, 4, 32, 800)])
 def test_few(gpu_lib, T, E, k, H, I):
     for rule, flags in ((M.FLOOR, 0), (M.CEIL, gpu_lib.NV4_RENORM)):
         x, lg, w, v13, v2 = few_case(gpu_lib, T, E, k, H, I, seed=T + H, rule=rule)

@@ -142,7 +142,8 @@ def _few(lib, **o):
     (EINVAL, dict(k=0)), (EUNSUPPORTED, dict(k=5)), (EUNSUPPORTED, dict(E=64, k=33)), (EINVAL, dict(fl=2)),
     (EINVAL, dict(lg=None, fl=1)), (EINVAL, dict(rule=2)), (EINVAL, dict(xt=2)), (EINVAL, dict(ot=2)),
     (EINVAL, dict(H=0)), (EALIGN, dict(H=80)), (EALIGN, dict(I=16)), (EINVAL, dict(w13=mx(4 * 32, 64))),
-    (EINVAL, dict(w13=None)), (EINVAL, dict(w2=mx(4 * 64, 64))), (EALIGN, dict(w2=mx(4 * 64, 32, codes=0x1004))),
+    (EINVAL, dict(w13=None)),
+    (EINVAL, dict(H=1 << 17, I=1 << 15, w13=mx(4 << 16, 1 << 17), w2=mx(4 << 17, 1 << 15))), (EINVAL, dict(w2=mx(4 * 64, 64))), (EALIGN, dict(w2=mx(4 * 64, 32, codes=0x1004))),
     (EINVAL, dict(x=None)), (EINVAL, dict(out=None)), (EINVAL, dict(lg=None)), (EINVAL, dict(lg=None, ids=P)),
     (EINVAL, dict(ldx=56)), (EINVAL, dict(ldo=63)), (EALIGN, dict(ldx=68)), (EALIGN, dict(x=ctypes.c_void_p(0x1004))),
     (EALIGN, dict(out=ctypes.c_void_p(0x1001))), (EWORKSPACE, dict(ws=None)), (EWORKSPACE, dict(wsb=100)),
