@@ -1,4 +1,4 @@
-// A whole MXFP4 expert layer for a few tokens (T <= 64, a decode step) in three kernels.
+// A whole MXFP4 expert layer for a few tokens (T <= 64, a decode step) in two or three kernels.
 //
 // At this size the layer is bound by reading the chosen experts' weights once (0.53 bytes per
 // element; 2.5 MB per expert at hidden size 2048 and expert size 768) and, below that, by
@@ -6,18 +6,19 @@
 // look-up only and are all under way at once, and no intermediate but the quantised rows.
 //
 //   1. k_few_route    routes the tokens (topk_device.h), a few per workgroup, and quantises x.
+//                     Left out for the smallest batches (few_fused): there every workgroup of
+//                     the next kernel routes and quantises for itself, in LDS.
 //   2. k_few_gate_up  one workgroup per (expert in use, 32 columns of I): gate and up products
 //                     for all the expert's tokens, SwiGLU and re-quantisation: 32 columns are
-//                     one MX block.  The K dimension is split over the four waves.  Each
-//                     workgroup finds its expert's rows itself from the T * k ids (a 64-bit
-//                     token mask gives their order without sorting); one more workgroup lists
-//                     all experts' rows for the next kernel meanwhile.
+//                     one MX block.  The K dimension is split over the eight waves.  Every wave
+//                     finds its expert's rows itself from the T * k ids (ballots, no sorting);
+//                     one more workgroup lists all experts' rows for the next kernel meanwhile.
 //   3. k_few_down     one workgroup per 16 columns of H: its waves walk over the experts, add
 //                     weight * product into a token table in LDS (one per wave), and the tables
-//                     are summed in wave order.  No atomics on sums: the result is
-//                     deterministic.
-// With at most 16 assignments (T * k) and no fewer experts nothing is grouped: every assignment
-// is taken as an expert with one row.
+//                     are summed in wave order.  Where there are few columns, several workgroups
+//                     share a tile's experts.  No atomics on sums: the result is deterministic.
+// An assignment (token t, choice j) is numbered f = j * T + t.  With at most 16 of them and no
+// fewer experts the last kernel groups nothing: every assignment is an expert with one row.
 //
 // Products: v_mfma_scale_f32_16x16x128_f8f6f4 with weight rows as the first operand and up to
 // 16 of the expert's tokens as the second, straight from global memory: lane (row, g) holds
@@ -29,6 +30,7 @@
 #include "mx_device.h"
 #include "mx_internal.h"
 #include "mx_rows.h"
+#include "nv4_internal.h"
 #include "topk_device.h"
 #include "../../include/nv4moe.h"
 
@@ -37,16 +39,20 @@ namespace {
 
 constexpr int kMaxT = 64;      // tokens (one bit each in an expert's mask)
 constexpr int kMaxE = 1024;
-constexpr int kMaxR = kMaxT * 32;
+constexpr int kMaxSplits = 4;  // workgroups that share a column tile of the down product
 constexpr int kDirect = 16;    // up to this many assignments are taken one by one
 constexpr uint32_t kOut = 0xFFFFFF00u;  // a byte offset behind every buffer
 
-// Workspace: per assignment f = t * k + j the expert (or -1) and its weight; the experts in use
-// with the start of their rows, and the rows' assignments; the quantised x and SwiGLU rows.
+// Workspace: per assignment f = j * T + t the expert (or -1) and its weight; the experts in use
+// with the start of their rows, and the rows' assignments; the down product's partial sums; the
+// quantised x and SwiGLU rows.
 struct FewWs {
   int32_t *id;
   float *w;
   int32_t *n_active, *act_e, *act_row, *row_f;
+  int32_t *offsets, *row_token;  // few_grouped: every expert's first row, the rows' tokens
+  int32_t *arrived;  // per column tile of the down product: workgroups that left their sums
+  float *sums;       // [tile][split][token][16]
   uint8_t *x_codes, *x_scales, *h_codes, *h_scales;
 };
 __host__ __device__ inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -66,6 +72,11 @@ __host__ __device__ inline size_t few_ws(void *base, int64_t T, int E, int k, in
   w.act_e = reinterpret_cast<int32_t *>(take(A * 4));
   w.act_row = reinterpret_cast<int32_t *>(take((A + 1) * 4));
   w.row_f = reinterpret_cast<int32_t *>(take(R * 4));
+  w.offsets = reinterpret_cast<int32_t *>(take((E + 1) * 4));
+  w.row_token = reinterpret_cast<int32_t *>(take(R * 4));
+  const int64_t tiles = (H + 15) / 16;
+  w.arrived = reinterpret_cast<int32_t *>(take(tiles * 4));
+  w.sums = reinterpret_cast<float *>(take(tiles * kMaxSplits * T * 16 * 4));
   w.x_codes = reinterpret_cast<uint8_t *>(take(T * (H / 2)));
   w.x_scales = reinterpret_cast<uint8_t *>(take(T * sc_stride(H)));
   w.h_codes = reinterpret_cast<uint8_t *>(take(R * (I / 2)));
@@ -75,6 +86,10 @@ __host__ __device__ inline size_t few_ws(void *base, int64_t T, int E, int k, in
 
 __host__ __device__ inline bool few_direct(const MxFewArgs &a) {
   return a.T * a.k <= kDirect && a.T * a.k <= a.E;
+}
+// token of an assignment: f mod T (f + 0.5 keeps the quotient away from an integer)
+__device__ __forceinline__ int few_token(int f, int T) {
+  return f - (int)(((float)f + 0.5f) * __builtin_amdgcn_rcpf((float)T)) * T;
 }
 
 // ---------------------------------------------------------------- 1. routing, x
@@ -120,29 +135,29 @@ __global__ __launch_bounds__(256) void k_few_route(MxFewArgs a, int nroute) {
     float w;
     const bool nan = topk_token<NPL, LPT>(a.logits + (int64_t)t * a.E, valid, a.E, a.k, a.flags, lane, sub, ll, id, w);
     if (valid && ll < a.k) {
-      const int f = t * a.k + ll;
+      const int f = ll * a.T + t;
       ws.id[f] = id < a.E ? id : -1;  // every remaining logit was NaN: no expert
       ws.w[f] = w;
-      if (a.topk_ids) a.topk_ids[f] = id;
-      if (a.topk_w) a.topk_w[f] = w;
+      if (a.topk_ids) a.topk_ids[t * a.k + ll] = id;
+      if (a.topk_w) a.topk_w[t * a.k + ll] = w;
     }
     if (nan && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDsNanLogit);
     return;
   }
   // the caller's ids may repeat within a token: the first takes the sum of the weights, in order
   const int R = a.T * a.k;
-  for (int f = blockIdx.x * 256 + tid; f < R; f += nroute * 256) {
-    const int f0 = f / a.k * a.k, id = a.topk_ids[f];
+  for (int i = blockIdx.x * 256 + tid; i < R; i += nroute * 256) {
+    const int t = i / a.k, j0 = i - t * a.k, id = a.topk_ids[i];
     const bool good = id >= 0 && id < a.E;
     bool first = true;
     float w = 0.0f;
-    for (int j = f0; j < f0 + a.k; ++j) {
-      if (a.topk_ids[j] != id) continue;
-      if (j < f) first = false;
-      w += a.topk_w[j];
+    for (int j = 0; j < a.k; ++j) {
+      if (a.topk_ids[t * a.k + j] != id) continue;
+      if (j < j0) first = false;
+      w += a.topk_w[t * a.k + j];
     }
-    ws.id[f] = good && first ? id : -1;
-    ws.w[f] = w;
+    ws.id[j0 * a.T + t] = good && first ? id : -1;
+    ws.w[j0 * a.T + t] = w;
     if (!good && a.dev_status) atomicOr(a.dev_status, kDsBadExpert);
   }
 }
@@ -150,11 +165,15 @@ __global__ __launch_bounds__(256) void k_few_route(MxFewArgs a, int nroute) {
 // ---------------------------------------------------------------- products
 
 // (device-only helpers: the buffer-resource type exists only on the GPU target)
-__device__ __forceinline__ int4 load16(const void *base, uint32_t bytes, uint32_t off) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4 load16(const void *base, uint32_t bytes, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), off, 0, 0);
-  return make_int4((int)v[0], (int)v[1], (int)v[2], (int)v[3]);
+}
+__device__ __forceinline__ u32x2 load8(const void *base, uint32_t bytes, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b64(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), off, 0, 0);
 }
 __device__ __forceinline__ uint32_t load1(const void *base, uint32_t bytes, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b8(
@@ -166,10 +185,6 @@ __device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *p) {
   return reinterpret_cast<const uint8_t *>(((uint64_t)hi << 32) | lo);
 }
 
-struct Frag {
-  int4 c;      // 32 codes
-  uint32_t s;  // their scale byte
-};
 // One matrix (or one expert's part of it): K = 32 nb
 struct Mat {
   const uint8_t *codes, *scales;
@@ -181,35 +196,57 @@ __device__ __forceinline__ Mat matrix(const uint8_t *codes, const uint8_t *scale
   return Mat{uniform_ptr(codes + row0 * (nb * 16)), uniform_ptr(scales + row0 * sld), rows * (uint32_t)(nb * 16),
              rows * (uint32_t)sld, nb, sld};
 }
-// block b of a row (row < 0: none); zeros behind K
-__device__ __forceinline__ Frag load_frag(const Mat &m, int row, int b) {
-  const bool live = row >= 0 && b < m.nb;
-  return Frag{load16(m.codes, m.cbytes, live ? (uint32_t)(row * m.nb + b) * 16u : kOut),
-              load1(m.scales, m.sbytes, live ? (uint32_t)(row * m.sld + b) : kOut)};
+// Block b of a row (row < 0: none): its 32 codes, and its scale byte; zeros behind K.
+__device__ __forceinline__ u32x4 load_codes(const Mat &m, int row, int b) {
+  return load16(m.codes, m.cbytes, row >= 0 && b < m.nb ? (uint32_t)(row * m.nb + b) * 16u : kOut);
 }
-__device__ __forceinline__ f32x4 mfma16(const Frag &a, const Frag &b, f32x4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{a.c.x, a.c.y, a.c.z, a.c.w, 0, 0, 0, 0},
-                                                          i32x8{b.c.x, b.c.y, b.c.z, b.c.w, 0, 0, 0, 0}, c, 4, 4, 0,
-                                                          (int)a.s, 0, (int)b.s);
+__device__ __forceinline__ uint32_t load_scale(const Mat &m, int row, int b) {
+  return load1(m.scales, m.sbytes, row >= 0 && b < m.nb ? (uint32_t)(row * m.sld + b) : kOut);
 }
-
+// The scale bytes of two consecutive steps (8 blocks from block b0, a multiple of 4) of a row:
+// dword i holds step i's four blocks, of which lane group g takes byte g (and b0 + 4 i + g < nb).
+__device__ __forceinline__ u32x2 load_scales2(const Mat &m, int row, int b0) {
+  return load8(m.scales, m.sbytes, row >= 0 && b0 < m.nb ? (uint32_t)(row * m.sld + b0) : kOut);
+}
+__device__ __forceinline__ uint32_t scale_of(uint32_t dword, int g, int b, int nb) {
+  return b < nb ? dword >> (8 * g) : 0u;
+}
+__device__ __forceinline__ i32x8 operand(u32x4 v) {  // FP4 reads the first four of eight dwords
+  return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
 // ---------------------------------------------------------------- 2. gate and up
 
-constexpr int kGuWaves = 4, kGuSteps = 4;  // steps of K = 128 a wave holds at a time
+constexpr int kGuWaves = 8, kGuSteps = 2;  // steps of K = 128 a wave holds at a time
+constexpr int kGuThreads = kGuWaves * 64;
 
-// The experts in use, the starts of their rows and the rows' assignments, for k_few_down.
-__device__ void list_experts(const MxFewArgs &a, const FewWs &ws, unsigned long long *mask, int *start, int *wsum) {
+constexpr int kFusedElems = 8192;                // tokens x H that a workgroup quantises for itself
+constexpr int kFusedTokens = 2;
+
+struct FewList {
+  unsigned long long mask[kMaxE];
+  int start[kMaxE];
+  int wsum[4];
+};
+// The experts in use, the starts of their rows and the rows' assignments, for k_few_down (and, for
+// few_grouped, all experts' starts and the rows' tokens); id: the assignments' experts.
+template <bool GROUPED>
+__device__ void list_experts(const MxFewArgs &a, const FewWs &ws, const int *id, FewList &sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, R = a.T * a.k;
-  for (int e = tid; e < kMaxE; e += 256) mask[e] = 0ull;
+  for (int e = tid; e < kMaxE; e += kGuThreads) sh.mask[e] = 0ull;
   __syncthreads();
-  for (int f = tid; f < R; f += 256)
-    if (ws.id[f] >= 0) atomicOr(&mask[ws.id[f]], 1ull << (f / a.k));
+  for (int f = tid; f < R; f += kGuThreads)
+    if (id[f] >= 0) atomicOr(&sh.mask[id[f]], 1ull << few_token(f, a.T));
   __syncthreads();
-  // exclusive prefix over the experts of (in use, rows), packed: both stay below 2^16
+  // exclusive prefix over the experts of (in use, rows), packed (both stay below 2^16): four
+  // experts for each of the first 256 threads
+  const bool mine = tid < kMaxE / 4;
   int own[4], sum = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int n = __popcll(mask[tid * 4 + i]);
+    const int n = mine ? __popcll(sh.mask[tid * 4 + i]) : 0;
     own[i] = n | (n ? 1 << 16 : 0);
     sum += own[i];
   }
@@ -219,114 +256,196 @@ __device__ void list_experts(const MxFewArgs &a, const FewWs &ws, unsigned long 
     const int x = __shfl_up(s, o, 64);
     if (lane >= o) s += x;
   }
-  if (lane == 63) wsum[wave] = s;
+  if (lane == 63 && mine) sh.wsum[wave] = s;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) s += wsum[w];
+  for (int w = 0; w < std::min(wave, 4); ++w) s += sh.wsum[w];
   int ex = s - sum;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    start[tid * 4 + i] = ex & 0xFFFF;
+    if (mine) sh.start[tid * 4 + i] = ex & 0xFFFF;
+    if (GROUPED && mine && tid * 4 + i <= a.E) ws.offsets[tid * 4 + i] = ex & 0xFFFF;
     if (own[i]) {
       ws.act_e[ex >> 16] = tid * 4 + i;
       ws.act_row[ex >> 16] = ex & 0xFFFF;
     }
     ex += own[i];
   }
-  if (tid == 255) {
+  if (tid == kMaxE / 4 - 1) {
     *ws.n_active = ex >> 16;
+    if (GROUPED && a.E == kMaxE) ws.offsets[kMaxE] = ex & 0xFFFF;
     ws.act_row[ex >> 16] = ex & 0xFFFF;
   }
   __syncthreads();
-  for (int f = tid; f < R; f += 256) {
-    const int id = ws.id[f];
-    if (id >= 0) ws.row_f[start[id] + __popcll(mask[id] & ((1ull << (f / a.k)) - 1ull))] = f;
+  for (int f = tid; f < R; f += kGuThreads) {
+    const int e = id[f];
+    if (e < 0) continue;
+    const int t = few_token(f, a.T), r = sh.start[e] + __popcll(sh.mask[e] & ((1ull << t) - 1ull));
+    ws.row_f[r] = f;
+    if (GROUPED) ws.row_token[r] = t;
   }
 }
 
-__global__ __launch_bounds__(kGuWaves * 64) void k_few_gate_up(MxFewArgs a) {
+// few_grouped: the rows' order, for the grouped GEMM that takes k_few_gate_up's place
+__global__ __launch_bounds__(kGuThreads) void k_few_group(MxFewArgs a) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
-  __shared__ union {
+  __shared__ FewList list;
+  for (int i = threadIdx.x; i < (a.H + 15) / 16; i += kGuThreads) ws.arrived[i] = 0;
+  list_experts<true>(a, ws, ws.id, list);
+}
+
+// FUSED (logits given, T <= kFusedTokens, T * H <= kFusedElems): routes and quantises x as well;
+// NPL, LPT as for topk_token, F32 the type of x.
+template <bool FUSED, int NPL, int LPT, bool F32>
+__global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
+  FewWs ws;
+  few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
+  union Shared {
     float part[kGuWaves][16][64];
-    struct {
-      unsigned long long mask[kMaxE];
-      int start[kMaxE];
-    } list;
-  } sh;
-  __shared__ unsigned long long smask;
-  __shared__ int rows[kMaxT];
-  __shared__ int wsum[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    FewList list;
+  };
+  __shared__ Shared sh;
+  __shared__ int rows[kGuWaves][kMaxT];  // one list per wave: no barrier between finding and using it
+  __shared__ int s_id[FUSED ? kFusedTokens * 32 : 1];
+  __shared__ float s_w[FUSED ? kFusedTokens * 32 : 1];
+  __shared__ __attribute__((aligned(16))) uint8_t s_xc[FUSED ? kFusedElems / 2 : 16];
+  __shared__ uint32_t s_xs[FUSED ? kFusedElems / 32 : 1];  // (a row of H = 32 has a whole dword)
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int R = a.T * a.k;
-  const bool direct = few_direct(a);
+  const int steps = (a.H + 127) / 128;
+  const int *id = ws.id;
+  if constexpr (FUSED) {
+    // the first waves route, the others quantise meanwhile
+    constexpr int TPW = kWave / LPT;
+    const int l16 = lane & 15, units = a.T * steps, nroute = (a.T + TPW - 1) / TPW;
+    for (int u0 = (wave - nroute) * 4; u0 < units && wave >= nroute; u0 += (kGuWaves - nroute) * 4) {
+      const int u = u0 + (lane >> 4), row = u / steps, seg = u - row * steps, col = seg * 128 + l16 * 8;
+      uint4 v[F32 ? 2 : 1];
+#pragma unroll
+      for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (row < a.T && col < a.H) {
+          const int64_t at = row * a.ldx + col;
+          v[i] = F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at)[i]
+                     : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)[i];
+        }
+      }
+      uint32_t c, d;
+      const bool bad = mx_unit<F32>(v, l16, a.ceil_rule, c, d);
+      if (row < a.T) {
+        if (col < a.H) *reinterpret_cast<uint32_t *>(s_xc + row * (a.H / 2) + col / 2) = c;
+        if (l16 == 0) s_xs[u] = d;
+      }
+      if (bad && a.dev_status && blockIdx.x == 0) atomicOr(a.dev_status, kDsNonFinite);
+    }
+    if (wave < nroute) {
+      const int sub = lane / LPT, ll = lane % LPT;
+      const int t = wave * TPW + sub;
+      const bool valid = t < a.T;
+      int e;
+      float w;
+      const bool nan = topk_token<NPL, LPT>(a.logits + (int64_t)t * a.E, valid, a.E, a.k, a.flags, lane, sub, ll, e, w);
+      if (valid && ll < a.k) {
+        s_id[ll * a.T + t] = e < a.E ? e : -1;
+        s_w[ll * a.T + t] = w;
+        if (blockIdx.x == 0) {
+          if (a.topk_ids) a.topk_ids[t * a.k + ll] = e;
+          if (a.topk_w) a.topk_w[t * a.k + ll] = w;
+        }
+      }
+      if (nan && lane == 0 && a.dev_status && blockIdx.x == 0) atomicOr(a.dev_status, kDsNanLogit);
+    }
+    __syncthreads();
+    id = s_id;
+  }
   if (blockIdx.x == 0) {
-    if (!direct) list_experts(a, ws, sh.list.mask, sh.list.start, wsum);
+    if constexpr (FUSED) {
+      for (int f = tid; f < R; f += kGuThreads) {
+        ws.id[f] = s_id[f];
+        ws.w[f] = s_w[f];
+      }
+    }
+    for (int i = tid; i < (a.H + 15) / 16; i += kGuThreads) ws.arrived[i] = 0;
+    if (!few_direct(a)) list_experts<false>(a, ws, id, sh.list);
     return;
   }
   const int tiles = a.I / 32;
   const int y = (int)(blockIdx.x - 1) / tiles, c0 = ((int)(blockIdx.x - 1) - y * tiles) * 32;
   // y counts assignments or, when there are fewer of them, experts
   const bool by_f = R <= a.E;
-  const int e = by_f ? __builtin_amdgcn_readfirstlane(ws.id[y]) : y;
+  const int e = by_f ? __builtin_amdgcn_readfirstlane(id[y]) : y;
   if (e < 0) return;
-  int n = 1;
-  if (direct) {
-    if (tid == 0) rows[0] = y;
-  } else {
-    if (tid == 0) smask = 0ull;
-    int mine[kMaxR / 256];
-    __syncthreads();
+  int n = 0, owner = -1;
+  for (int f0 = 0; f0 < R; f0 += 512) {
+    int ids[8];  // all under way at once
 #pragma unroll
-    for (int i = 0; i < kMaxR / 256; ++i) {
-      const int f = tid + i * 256;
-      mine[i] = f < R && ws.id[f] == e ? f / a.k : -1;
+    for (int c = 0; c < 8; ++c) ids[c] = id[std::min(f0 + c * 64 + lane, R - 1)];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int f = f0 + c * 64 + lane;
+      const bool hit = f < R && ids[c] == e;
+      const unsigned long long m = __ballot(hit);
+      if (hit) rows[wave][n + __popcll(m & ((1ull << lane) - 1ull))] = f;
+      if (m && owner < 0) owner = f0 + c * 64 + __builtin_ctzll(m);
+      n += __popcll(m);
     }
-#pragma unroll
-    for (int i = 0; i < kMaxR / 256; ++i)
-      if (mine[i] >= 0) atomicOr(&smask, 1ull << mine[i]);
-    __syncthreads();
-    const unsigned long long m = smask;
-    // nobody's expert, or an earlier assignment's workgroup has it
-    if (m == 0ull || (by_f && y / a.k != __builtin_ctzll(m))) return;
-#pragma unroll
-    for (int i = 0; i < kMaxR / 256; ++i)
-      if (mine[i] >= 0) rows[__popcll(m & ((1ull << mine[i]) - 1ull))] = tid + i * 256;
-    n = __builtin_amdgcn_readfirstlane(__popcll(m));
   }
+  n = __builtin_amdgcn_readfirstlane(n);
+  // nobody's expert, or an earlier assignment's workgroup has it
+  if (n == 0 || (by_f && owner != y)) return;
   const int l = lane & 15, g = lane >> 4;
   const Mat w13 = matrix(a.w13_codes, a.w13_scales, (int64_t)e * 2 * a.I, 2 * a.I, a.H);
   const Mat x = matrix(ws.x_codes, ws.x_scales, 0, a.T, a.H);
-  const int steps = (a.H + 127) / 128;
   const int per = min(kGuSteps, (steps + kGuWaves - 1) / kGuWaves);  // consecutive steps of a wave
   const int chunk = per * kGuWaves;
   // tiles: gate columns c0.., c0 + 16.., then the up rows
-  Frag w[kGuSteps][4];
+  static_assert(kGuSteps == 2, "load_scales2");
+  u32x4 w[kGuSteps][4];
+  u32x2 wsc[4];
   const auto load_w = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kGuSteps; ++i)
+    for (int t = 0; t < 4; ++t) {
+      const int row = c0 + (t & 1) * 16 + (t >> 1) * a.I + l;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        w[i][t] = load_frag(w13, i < per ? c0 + (t & 1) * 16 + (t >> 1) * a.I + l : -1, (s0 + i) * 4 + g);
+      for (int i = 0; i < kGuSteps; ++i) w[i][t] = load_codes(w13, i < per ? row : -1, (s0 + i) * 4 + g);
+      wsc[t] = load_scales2(w13, row, s0 * 4);
+    }
   };
   load_w(wave * per);
-  __syncthreads();  // the row list
   const int slot = tid >> 4, cc = (tid & 15) * 2;
   const int hsld = sc_stride(a.I);
   bool bad = false;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
   for (int q = 0; q < n; q += 16) {
-    const int tok = q + l < n ? rows[q + l] / a.k : -1;
+    const int tok = q + l < n ? few_token(rows[wave][q + l], a.T) : -1;
     f32x4 acc[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
     for (int c = 0; c < steps; c += chunk) {
-      if (c > 0 || (q > 0 && steps > chunk)) load_w(c + wave * per);  // otherwise the registers hold it
-      Frag xf[kGuSteps];
+      const int s0 = c + wave * per;
+      if (c > 0 || (q > 0 && steps > chunk)) load_w(s0);  // otherwise the registers hold it
+      u32x4 xc[kGuSteps];
+      uint32_t xs[kGuSteps];
 #pragma unroll
-      for (int i = 0; i < kGuSteps; ++i) xf[i] = load_frag(x, i < per ? tok : -1, (c + wave * per + i) * 4 + g);
+      for (int i = 0; i < kGuSteps; ++i) {
+        const int b = (s0 + i) * 4 + g;
+        if constexpr (FUSED) {
+          const bool live = tok >= 0 && i < per && b < x.nb;
+          xc[i] = live ? *reinterpret_cast<const u32x4 *>(s_xc + (tok * x.nb + b) * 16) : u32x4{0, 0, 0, 0};
+          xs[i] = live ? s_xs[tok * steps + s0 + i] >> (8 * g) : 0u;
+        } else {
+          xc[i] = load_codes(x, i < per ? tok : -1, b);
+          xs[i] = load_scale(x, i < per ? tok : -1, b);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < kGuSteps; ++i)
+      for (int i = 0; i < kGuSteps; ++i) {
+        const int b = (s0 + i) * 4 + g;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = mfma16(w[i][t], xf[i], acc[t]);
+        for (int t = 0; t < 4; ++t)
+          acc[t] = mfma16(w[i][t], scale_of(wsc[t][i], g, i < per ? b : x.nb, x.nb), xc[i], xs[i], acc[t]);
+      }
     }
     // sum over the waves, SwiGLU, re-quantise: thread = token slot of 16, two columns
     if (q) __syncthreads();
@@ -335,30 +454,32 @@ __global__ __launch_bounds__(kGuWaves * 64) void k_few_gate_up(MxFewArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) sh.part[wave][t * 4 + r][lane] = acc[t][r];
     __syncthreads();
-    // column c sits in tile c / 16, lane (c % 16) / 4 * 16 + slot, register c % 4
-    float h[2];
+    if (tid < 256) {
+      // column c sits in tile c / 16, lane (c % 16) / 4 * 16 + slot, register c % 4
+      float h[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = cc + u, reg = (c >> 4) * 4 + (c & 3), at = ((c & 15) >> 2) * 16 + slot;
-      float gate = 0, up = 0;
+      for (int u = 0; u < 2; ++u) {
+        const int c = cc + u, reg = (c >> 4) * 4 + (c & 3), at = ((c & 15) >> 2) * 16 + slot;
+        float gate = 0, up = 0;
 #pragma unroll
-      for (int v = 0; v < kGuWaves; ++v) {
-        gate += sh.part[v][reg][at];
-        up += sh.part[v][reg + 8][at];
+        for (int v = 0; v < kGuWaves; ++v) {
+          gate += sh.part[v][reg][at];
+          up += sh.part[v][reg + 8][at];
+        }
+        h[u] = gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
       }
-      h[u] = gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
-    }
-    uint32_t m = max(__float_as_uint(h[0]) & 0x7FFFFFFFu, __float_as_uint(h[1]) & 0x7FFFFFFFu);
-    m = oct_umax(m);
-    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, false));  // row_mirror
-    const uint32_t byte = mx_scale_byte(m, a.ceil_rule);
-    uint32_t c = mx_pack_f32<0>(0u, h[0], h[1], mx_scale_value(byte));
-    if (byte == kMxNan) c = 0u;
-    if (q + slot < n) {
-      bad |= byte == kMxNan;
-      const int64_t r = rows[q + slot];
-      ws.h_codes[r * (a.I / 2) + (c0 + cc) / 2] = (uint8_t)c;
-      if ((tid & 15) == 0) ws.h_scales[r * hsld + c0 / 32] = (uint8_t)byte;
+      uint32_t m = max(__float_as_uint(h[0]) & 0x7FFFFFFFu, __float_as_uint(h[1]) & 0x7FFFFFFFu);
+      m = oct_umax(m);
+      m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, false));  // row_mirror
+      const uint32_t byte = mx_scale_byte(m, a.ceil_rule);
+      uint32_t c = mx_pack_f32<0>(0u, h[0], h[1], mx_scale_value(byte));
+      if (byte == kMxNan) c = 0u;
+      if (q + slot < n) {
+        bad |= byte == kMxNan;
+        const int64_t r = rows[wave][q + slot];
+        ws.h_codes[r * (a.I / 2) + (c0 + cc) / 2] = (uint8_t)c;
+        if ((tid & 15) == 0) ws.h_scales[r * hsld + c0 / 32] = (uint8_t)byte;
+      }
     }
   }
   if (bad && a.dev_status) atomicOr(a.dev_status, kDsNonFinite);
@@ -368,111 +489,195 @@ __global__ __launch_bounds__(kGuWaves * 64) void k_few_gate_up(MxFewArgs a) {
 
 constexpr int kDnWaves = 16, kDnSteps = 6;
 
-// A wave's share: entries (experts in use, or assignments) wave / parts, + 16 / parts, ..; of
-// each the steps part, part + parts, ..  (parts > 1 with fewer than 16 entries).  The weights of
-// the next entry are loaded while this one is computed.
+// Workgroup (column tile, split): the tile's entries (experts in use, or assignments) are dealt to
+// the waves of its `splits` workgroups in turn.  Of an entry a wave takes the steps part,
+// part + parts, .. (parts > 1 with fewer than 16 entries).  The row numbers of the next entry are
+// loaded while this one is computed.  (Its weights too would take the kernel over 128 registers,
+// that is, to half the waves.)
+// With several splits each workgroup leaves its sums in the workspace, and the last one to
+// arrive adds them up, in split order whoever it is.
+// The SwiGLU rows are in assignment order, or (grouped) in expert order.
 template <bool OUT_F32>
-__global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a) {
+__global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int splits, int grouped) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
   extern __shared__ float table[];  // [wave][token][16 columns]
+  __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int R = a.T * a.k;
-  const bool direct = few_direct(a);
+  const bool direct = !grouped && few_direct(a);
   const int na = direct ? R : __builtin_amdgcn_readfirstlane(*ws.n_active);
-  const int parts = na > 8 ? 1 : na > 4 ? 2 : 4;
-  const int part = wave % parts, stride = kDnWaves / parts;
+  const int parts = na > 8 || splits > 1 ? 1 : na > 4 ? 2 : 4;
+  const int tile = blockIdx.x / splits, split = blockIdx.x - tile * splits;
+  const int part = wave % parts, stride = splits * kDnWaves / parts;
   const int steps = (a.I + 127) / 128;
-  const int c0 = blockIdx.x * 16;
+  const int c0 = tile * 16;
   const int wrow = c0 + l < a.H ? c0 + l : -1;
   const Mat h = matrix(ws.h_codes, ws.h_scales, 0, R, a.I);
   float *mine = table + wave * a.T * 16;
-  struct Entry {
-    int e, r0, n;
-  };
-  const auto entry = [&](int i) __attribute__((always_inline)) {
-    Entry n{-1, 0, 0};
-    if (i < na) {
-      if (direct) {
-        n = Entry{ws.id[i], i, 1};
-      } else {
-        n.e = ws.act_e[i];
-        n.r0 = ws.act_row[i];
-        n.n = ws.act_row[i + 1] - n.r0;
-      }
+  // the wave's entries, one per lane (at most 1024 / 16 of them): expert, first row, rows
+  int le = -1, lr = 0, ln = 0;
+  const int i0 = (split * kDnWaves + wave) / parts + lane * stride;
+  if (i0 < na) {
+    if (direct) {
+      le = ws.id[i0];
+      lr = i0;
+      ln = le < 0 ? 0 : 1;
+    } else {
+      le = ws.act_e[i0];
+      lr = ws.act_row[i0];
+      ln = ws.act_row[i0 + 1] - lr;
     }
-    n.e = __builtin_amdgcn_readfirstlane(n.e);
-    n.r0 = __builtin_amdgcn_readfirstlane(n.r0);
-    n.n = __builtin_amdgcn_readfirstlane(n.e < 0 ? 0 : n.n);
-    return n;
-  };
-  Frag w[kDnSteps];
-  const auto load_w = [&](const Entry &n, int s0) __attribute__((always_inline)) {
-    const Mat w2 = matrix(a.w2_codes, a.w2_scales, (int64_t)max(n.e, 0) * a.H, a.H, a.I);
-#pragma unroll
-    for (int s = 0; s < kDnSteps; ++s) w[s] = load_frag(w2, n.e < 0 ? -1 : wrow, (s0 + s * parts) * 4 + g);
-  };
-  Entry cur = entry(wave / parts);
-  load_w(cur, part);
+  }
+  const int count = __popcll(__ballot(i0 < na));
   for (int i = lane; i < a.T * 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
-  for (int i = wave / parts; i < na; i += stride) {
-    const Entry next = entry(i + stride);
-    const bool once = steps <= parts * kDnSteps;  // the registers hold the whole row
-    for (int q = 0; q < cur.n; q += 16) {
-      const int f = q + l < cur.n ? (direct ? cur.r0 : ws.row_f[cur.r0 + q + l]) : -1;
+  const auto load_w = [&](u32x4 (&wc)[kDnSteps], uint32_t (&wsc)[kDnSteps], int e, int s0) __attribute__((always_inline)) {
+    const Mat w2 = matrix(a.w2_codes, a.w2_scales, (int64_t)max(e, 0) * a.H, a.H, a.I);
+#pragma unroll
+    for (int s = 0; s < kDnSteps; ++s) {
+      wc[s] = load_codes(w2, e < 0 ? -1 : wrow, (s0 + s * parts) * 4 + g);
+      wsc[s] = load_scale(w2, e < 0 ? -1 : wrow, (s0 + s * parts) * 4 + g);
+    }
+  };
+  const auto row_of = [&](int r0, int n, int q) __attribute__((always_inline)) {  // assignment of row slot q + l, or -1
+    return q + l < n ? (direct ? r0 : ws.row_f[r0 + q + l]) : -1;
+  };
+  u32x4 w[kDnSteps];
+  uint32_t wsc[kDnSteps];
+  int e = __builtin_amdgcn_readlane(le, 0), r0 = __builtin_amdgcn_readlane(lr, 0), n = __builtin_amdgcn_readlane(ln, 0);
+  load_w(w, wsc, e, part);
+  int f = row_of(r0, n, 0);
+  const bool once = steps <= parts * kDnSteps;  // the registers hold the whole row
+  for (int c = 0; c < count; ++c) {
+    const int c1 = min(c + 1, 63);
+    const bool more = c + 1 < count;
+    const int e1 = more ? __builtin_amdgcn_readlane(le, c1) : -1, r1 = __builtin_amdgcn_readlane(lr, c1);
+    const int n1 = more ? __builtin_amdgcn_readlane(ln, c1) : 0;
+    const int f1 = row_of(r1, n1, 0);
+    for (int q = 0; q < n; q += 16) {
+      if (q > 0) f = row_of(r0, n, q);
       const float wt = f >= 0 ? ws.w[f] : 0.0f;
+      const int hr = !grouped ? f : q + l < n ? r0 + q + l : -1;
       f32x4 acc = f32x4{0, 0, 0, 0};
       for (int s0 = part; s0 < steps; s0 += parts * kDnSteps) {
-        if (!once && (s0 != part || q > 0)) load_w(cur, s0);
-        Frag x[kDnSteps];
+        if (!once && (s0 != part || q > 0)) load_w(w, wsc, e, s0);
+        u32x4 x[kDnSteps];
+        uint32_t xs[kDnSteps];
 #pragma unroll
-        for (int s = 0; s < kDnSteps; ++s) x[s] = load_frag(h, f, (s0 + s * parts) * 4 + g);
+        for (int s = 0; s < kDnSteps; ++s) {
+          x[s] = load_codes(h, hr, (s0 + s * parts) * 4 + g);
+          xs[s] = load_scale(h, hr, (s0 + s * parts) * 4 + g);
+        }
 #pragma unroll
-        for (int s = 0; s < kDnSteps; ++s) acc = mfma16(w[s], x[s], acc);
+        for (int s = 0; s < kDnSteps; ++s) acc = mfma16(w[s], wsc[s], x[s], xs[s], acc);
       }
       // lane = row slot l, columns 4 g ..: an expert's rows are different tokens, so no two
       // lanes meet in the table
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       if (f >= 0) {
-        f32x4 *p = reinterpret_cast<f32x4 *>(mine + f / a.k * 16 + g * 4);
+        f32x4 *p = reinterpret_cast<f32x4 *>(mine + few_token(f, a.T) * 16 + g * 4);
         f32x4 v = *p;
 #pragma unroll
         for (int u = 0; u < 4; ++u) v[u] += wt * acc[u];
         *p = v;
       }
     }
-    load_w(next, part);
-    cur = next;
+    e = e1;
+    r0 = r1;
+    n = n1;
+    f = f1;
+    if (more) load_w(w, wsc, e, part);
   }
   __syncthreads();
-  for (int i = tid; i < a.T * 16; i += kDnWaves * 64) {
-    float s = 0;
-#pragma unroll
-    for (int v = 0; v < kDnWaves; ++v) s += table[v * a.T * 16 + i];
+  const auto store = [&](int i, float v) __attribute__((always_inline)) {
     const int t = i >> 4, c = c0 + (i & 15);
     if (c < a.H) {
-      if constexpr (OUT_F32) static_cast<float *>(a.out)[t * a.ldo + c] = s;
-      else reinterpret_cast<__bf16 *>(a.out)[t * a.ldo + c] = (__bf16)s;
+      if constexpr (OUT_F32) static_cast<float *>(a.out)[t * a.ldo + c] = v;
+      else reinterpret_cast<__bf16 *>(a.out)[t * a.ldo + c] = (__bf16)v;
     }
+  };
+  float *sums = ws.sums + (int64_t)tile * splits * a.T * 16;
+  for (int i = tid; i < a.T * 16; i += kDnWaves * 64) {
+    float v = 0;
+#pragma unroll
+    for (int k = 0; k < kDnWaves; ++k) v += table[k * a.T * 16 + i];
+    if (splits == 1) store(i, v);
+    else __hip_atomic_store(sums + split * a.T * 16 + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (splits == 1) return;
+  // The sums were stored past this XCD's L2 and are loaded past the reader's (agent scope): it is
+  // enough that they have arrived before this workgroup counts as arrived.  A fence at that scope
+  // would write back and invalidate the whole L2.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0)
+    s_last = __hip_atomic_fetch_add(ws.arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int i = tid; i < a.T * 16; i += kDnWaves * 64) {
+    float v = 0;
+    for (int k = 0; k < splits; ++k)
+      v += __hip_atomic_load(sums + k * a.T * 16 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    store(i, v);
   }
 }
 
+// Batches with more assignments than this go through the grouped GEMM (see the top).
+constexpr int kGroupedRows = 72;
+bool few_grouped(const MxFewArgs &a) { return a.T * a.k > kGroupedRows; }
+
+// The smallest batches: one kernel less (see the top).
+bool few_fused(const MxFewArgs &a) {
+  return a.logits && a.T <= kFusedTokens && (int64_t)a.T * a.H <= kFusedElems;
+}
+
 template <int NPL, int LPT, bool F32>
-void launch_route(const MxFewArgs &a, hipStream_t stream) {
+hipError_t launch_first(const MxFewArgs &a, hipStream_t stream) {
+  const unsigned grid = 1 + (unsigned)(a.I / 32) * (unsigned)std::min(a.E, a.T * a.k);  // experts in use
+  if (few_fused(a)) {
+    k_few_gate_up<true, NPL, LPT, F32><<<grid, kGuThreads, 0, stream>>>(a);
+    return hipSuccess;
+  }
   const int per = 4 * (kWave / LPT);  // tokens per routing workgroup
   const int nroute = a.logits ? (a.T + per - 1) / per : (a.T * a.k + 255) / 256;
   const int units = a.T * ((a.H + 127) / 128);
   k_few_route<NPL, LPT, F32><<<(unsigned)(nroute + (units + 15) / 16), 256, 0, stream>>>(a, nroute);
+  if (!few_grouped(a)) {
+    k_few_gate_up<false, 1, 64, false><<<grid, kGuThreads, 0, stream>>>(a);
+    return hipSuccess;
+  }
+  k_few_group<<<1, kGuThreads, 0, stream>>>(a);
+  FewWs ws;
+  few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
+  MxGemmArgs g{};
+  g.a_codes = ws.x_codes;
+  g.a_scales = ws.x_scales;
+  g.a_rows = a.T;
+  g.K = a.H;
+  g.a_rows_index = ws.row_token;
+  g.b_codes = a.w13_codes;
+  g.b_scales = a.w13_scales;
+  g.b_rows = (int64_t)a.E * 2 * a.I;
+  g.offsets = ws.offsets;
+  g.E = a.E;
+  g.M_cap = a.T * a.k;
+  g.N = a.I;
+  g.group_mode = NV4_GROUP_M;
+  g.epilogue = NV4_EPI_SWIGLU;
+  g.q_codes = ws.h_codes;
+  g.q_scales = ws.h_scales;
+  g.ceil_rule = a.ceil_rule;
+  return launch_mx_gemm(g, stream);
 }
 template <bool F32>
-void launch_route(const MxFewArgs &a, hipStream_t stream) {
-  if (a.E <= 64) launch_route<2, 32, F32>(a, stream);
-  else if (a.E <= 128) launch_route<4, 32, F32>(a, stream);
-  else if (a.E <= 256) launch_route<4, 64, F32>(a, stream);
-  else if (a.E <= 512) launch_route<8, 64, F32>(a, stream);
-  else launch_route<16, 64, F32>(a, stream);
+hipError_t launch_first(const MxFewArgs &a, hipStream_t stream) {
+  if (a.E <= 64) return launch_first<2, 32, F32>(a, stream);
+  if (a.E <= 128) return launch_first<4, 32, F32>(a, stream);
+  if (a.E <= 256) return launch_first<4, 64, F32>(a, stream);
+  if (a.E <= 512) return launch_first<8, 64, F32>(a, stream);
+  return launch_first<16, 64, F32>(a, stream);
 }
 
 }  // namespace
@@ -484,13 +689,15 @@ size_t mx_few_workspace_bytes(int64_t T, int E, int k, int64_t H, int64_t I) {
 
 hipError_t launch_mx_few(const MxFewArgs &a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  if (a.x_is_f32) launch_route<true>(a, stream); else launch_route<false>(a, stream);
-  const int most = std::min(a.E, a.T * a.k);  // experts in use
-  k_few_gate_up<<<1 + (unsigned)(a.I / 32) * (unsigned)most, kGuWaves * 64, 0, stream>>>(a);
+  const hipError_t first = a.x_is_f32 ? launch_first<true>(a, stream) : launch_first<false>(a, stream);
+  if (first != hipSuccess) return first;
   const unsigned lds = (unsigned)(kDnWaves * a.T * 16 * sizeof(float));
-  const unsigned grid = (unsigned)((a.H + 15) / 16);
-  if (a.out_is_f32) k_few_down<true><<<grid, kDnWaves * 64, lds, stream>>>(a);
-  else k_few_down<false><<<grid, kDnWaves * 64, lds, stream>>>(a);
+  const int tiles = (a.H + 15) / 16, entries = std::min(a.E, a.T * a.k);
+  // workgroups for the whole chip, at least an entry for each of their waves
+  const int splits = std::max(1, std::min({kMaxSplits, device_cu_count() / tiles, entries / kDnWaves}));
+  const unsigned grid = (unsigned)(tiles * splits);
+  if (a.out_is_f32) k_few_down<true><<<grid, kDnWaves * 64, lds, stream>>>(a, splits, few_grouped(a));
+  else k_few_down<false><<<grid, kDnWaves * 64, lds, stream>>>(a, splits, few_grouped(a));
   return hipGetLastError();
 }
 

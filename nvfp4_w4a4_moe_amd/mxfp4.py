@@ -16,6 +16,7 @@ package's top level.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -107,23 +108,29 @@ def _ints(t: torch.Tensor | None, name: str, n: int | None = None):
     return t.data_ptr()
 
 
+# the device's current stream as an address, without the Stream object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 class _Call:
     """One call's device and stream: every tensor has to be on the device of the first one, the
     launch goes to the given stream or to that device's current one, and temporaries stay
     alive for that stream."""
 
+    __slots__ = ("index", "device", "given", "stream")
+
     def __init__(self, stream, first: torch.Tensor, *others):
-        dev = first.device
+        index = first.get_device()
         for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device} in one call")
-        if dev.type != "cuda":
-            raise ValueError(f"tensors must be on a GPU, not on {dev}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-        self.device = dev
-        self.given = stream
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+        self.device = first.device
+        if index < 0 or self.device.type != "cuda":
+            raise ValueError(f"tensors must be on a GPU, not on {first.device}")
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
+        self.index, self.given = index, stream
+        self.stream = _raw_stream(index) if stream is None else stream.cuda_stream
 
     def empty(self, shape, dtype) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=self.device)
@@ -136,10 +143,10 @@ class _Call:
                      rows, K)
 
     def __call__(self, fn, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if torch.cuda.current_device() == self.index:
             status = fn(*args, self.stream)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.index):
                 status = fn(*args, self.stream)
         if status:
             _check(status)
@@ -147,6 +154,11 @@ class _Call:
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _few_workspace(T: int, E: int, k: int, H: int, I: int) -> int:
+    return load().mx_moe_few_workspace(T, E, k, H, I)
 
 
 # ----------------------------------------------------------------------------- quantisation
@@ -204,7 +216,7 @@ def mxfp4_dequantize(q: MXFP4, out_dtype=torch.bfloat16, out: torch.Tensor | Non
     if out is None:
         out = call.empty((q.rows, q.K), out_dtype)
     ldo = _matrix(out, "out")
-    if tuple(out.shape) != (q.rows, q.K):
+    if out.shape != (q.rows, q.K):
         raise ValueError(f"out must be [{q.rows}, {q.K}]")
     call(load().mxfp4_dequantize, q.c(), out.data_ptr(), _float(out, "out"), ldo)
     return out
@@ -411,21 +423,19 @@ def mx_moe_few(x: torch.Tensor, logits: torch.Tensor | None, w: MXExpertWeights,
     if H != w.H:
         raise ValueError(f"x has {H} columns, the weights {w.H}")
     if logits is not None and (logits.dtype != torch.float32 or not logits.is_contiguous() or
-                               tuple(logits.shape) != (T, w.E)):
+                               logits.shape != (T, w.E)):
         raise ValueError(f"logits must be contiguous FP32 [{T}, {w.E}]")
     if topk_w is not None and (topk_w.dtype != torch.float32 or not topk_w.is_contiguous() or topk_w.numel() != T * k):
         raise ValueError(f"topk_w must be contiguous FP32 [{T}, {k}]")
     if out is None:
         out = call.empty((T, H), out_dtype)
-    elif tuple(out.shape) != (T, H):
+    elif out.shape != x.shape:
         raise ValueError(f"out must be [{T}, {H}]")
-    lib = load()
-    need = lib.mx_moe_few_workspace(T, w.E, k, H, w.I)
     if ws is None:
-        ws = call.empty((max(need, 256),), torch.uint8)
+        ws = call.empty(max(_few_workspace(T, w.E, k, H, w.I), 256), torch.uint8)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be contiguous uint8")
-    call(lib.mx_moe_few, x.data_ptr(), _float(x, "x"), ldx, _p(logits), T, w.E, k, flags,
+    call(load().mx_moe_few, x.data_ptr(), _float(x, "x"), ldx, _p(logits), T, w.E, k, flags,
          _ints(topk_ids, "topk_ids", T * k), _p(topk_w), w.w13.c(), w.w2.c(), H, w.I, rule, out.data_ptr(),
          _float(out, "out"), _matrix(out, "out"), ws.data_ptr(), ws.numel(), _ints(dev_status, "dev_status"))
     return out
