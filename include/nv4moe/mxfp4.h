@@ -57,7 +57,7 @@ int64_t mxfp4_scale_stride(int64_t K);
 
 /*
  * mxfp4_quantize -- MXFP4 quantisation of a BF16 or FP32 matrix, one pass over it.
- *   x, xtype, x_rows, ldx  input [x_rows][ldx] (ldx >= K)
+ *   x, xtype, x_rows, ldx  input [x_rows][ldx] (ldx >= K; at most 2^22 in the column layouts)
  *   rows, K          logical rows (after the gather) and columns, K % 32 == 0
  *   row_index        device int32 [rows] or NULL (not with NV4_COLS_BATCHED): logical row
  *                    r is row row_index[r] of x; an index outside x is clamped into it

@@ -92,6 +92,8 @@ nv4_status mxfp4_quantize(const void *x, nv4_dtype xtype, int64_t x_rows, int64_
   if (layout != NV4_ROWS) {
     const int64_t chunks = layout == NV4_COLS_BATCHED ? nseg * ((rows / nseg + 127) / 128) : out->K / 128;
     if (chunks * ((K + 127) / 128) >= kMost32 / 2) return fail(NV4_EINVAL, "%s: shape too large", fn);
+    // a tile of 128 rows is addressed with 32-bit offsets
+    if (ldx > (1ll << 22)) return fail(NV4_EINVAL, "%s: ldx is above 2^22 in a column layout", fn);
   }
   nv4::MxQuantArgs a{};
   a.x = x;

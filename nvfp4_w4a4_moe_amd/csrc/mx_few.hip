@@ -40,7 +40,6 @@ namespace {
 constexpr int kMaxT = 64;      // tokens (one bit each in an expert's mask)
 constexpr int kMaxE = 1024;
 constexpr int kMaxSplits = 4;  // workgroups that share a column tile of the down product
-constexpr int kDirect = 16;    // up to this many assignments are taken one by one
 constexpr uint32_t kOut = 0xFFFFFF00u;  // a byte offset behind every buffer
 
 // Workspace: per assignment f = j * T + t the expert (or -1) and its weight; the experts in use
@@ -84,9 +83,6 @@ __host__ __device__ inline size_t few_ws(void *base, int64_t T, int E, int k, in
   return at;
 }
 
-__host__ __device__ inline bool few_direct(const MxFewArgs &a) {
-  return a.T * a.k <= kDirect && a.T * a.k <= a.E;
-}
 // token of an assignment: f mod T (f + 0.5 keeps the quotient away from an integer)
 __device__ __forceinline__ int few_token(int f, int T) {
   return f - (int)(((float)f + 0.5f) * __builtin_amdgcn_rcpf((float)T)) * T;
@@ -101,6 +97,8 @@ __global__ __launch_bounds__(256) void k_few_route(MxFewArgs a, int nroute) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x == gridDim.x - 1)
+    for (int i = tid; i < (a.H + 15) / 16; i += 256) ws.arrived[i] = 0;
   if ((int)blockIdx.x >= nroute) {
     const int l16 = lane & 15, spr = (a.H + 127) / 128;
     const int unit = (blockIdx.x - nroute) * 16 + (tid >> 4);
@@ -175,10 +173,6 @@ __device__ __forceinline__ u32x2 load8(const void *base, uint32_t bytes, uint32_
   return __builtin_amdgcn_raw_buffer_load_b64(
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), off, 0, 0);
 }
-__device__ __forceinline__ uint32_t load1(const void *base, uint32_t bytes, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b8(
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), off, 0, 0);
-}
 __device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
@@ -196,12 +190,9 @@ __device__ __forceinline__ Mat matrix(const uint8_t *codes, const uint8_t *scale
   return Mat{uniform_ptr(codes + row0 * (nb * 16)), uniform_ptr(scales + row0 * sld), rows * (uint32_t)(nb * 16),
              rows * (uint32_t)sld, nb, sld};
 }
-// Block b of a row (row < 0: none): its 32 codes, and its scale byte; zeros behind K.
+// Block b of a row (row < 0: none): its 32 codes; zeros behind K.
 __device__ __forceinline__ u32x4 load_codes(const Mat &m, int row, int b) {
   return load16(m.codes, m.cbytes, row >= 0 && b < m.nb ? (uint32_t)(row * m.nb + b) * 16u : kOut);
-}
-__device__ __forceinline__ uint32_t load_scale(const Mat &m, int row, int b) {
-  return load1(m.scales, m.sbytes, row >= 0 && b < m.nb ? (uint32_t)(row * m.sld + b) : kOut);
 }
 // The scale bytes of two consecutive steps (8 blocks from block b0, a multiple of 4) of a row:
 // dword i holds step i's four blocks, of which lane group g takes byte g (and b0 + 4 i + g < nb).
@@ -222,6 +213,9 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t 
 constexpr int kGuWaves = 8, kGuSteps = 2;  // steps of K = 128 a wave holds at a time
 constexpr int kGuThreads = kGuWaves * 64;
 
+// Batches with more assignments than this go through the grouped GEMM (see the top).
+constexpr int kGroupedRows = 72;
+constexpr int kIdChunks = (kGroupedRows + 63) / 64;
 constexpr int kFusedElems = 8192;                // tokens x H that a workgroup quantises for itself
 constexpr int kFusedTokens = 2;
 
@@ -230,10 +224,13 @@ struct FewList {
   int start[kMaxE];
   int wsum[4];
 };
-// The experts in use, the starts of their rows and the rows' assignments, for k_few_down (and, for
-// few_grouped, all experts' starts and the rows' tokens); id: the assignments' experts.
-template <bool GROUPED>
-__device__ void list_experts(const MxFewArgs &a, const FewWs &ws, const int *id, FewList &sh) {
+// few_grouped: the experts in use, all experts' first rows, the rows' assignments and tokens, for the
+// grouped GEMM that takes k_few_gate_up's place and for k_few_down.
+__global__ __launch_bounds__(kGuThreads) void k_few_group(MxFewArgs a) {
+  FewWs ws;
+  few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
+  __shared__ FewList sh;
+  const int *id = ws.id;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, R = a.T * a.k;
   for (int e = tid; e < kMaxE; e += kGuThreads) sh.mask[e] = 0ull;
   __syncthreads();
@@ -263,7 +260,7 @@ __device__ void list_experts(const MxFewArgs &a, const FewWs &ws, const int *id,
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (mine) sh.start[tid * 4 + i] = ex & 0xFFFF;
-    if (GROUPED && mine && tid * 4 + i <= a.E) ws.offsets[tid * 4 + i] = ex & 0xFFFF;
+    if (mine && tid * 4 + i <= a.E) ws.offsets[tid * 4 + i] = ex & 0xFFFF;
     if (own[i]) {
       ws.act_e[ex >> 16] = tid * 4 + i;
       ws.act_row[ex >> 16] = ex & 0xFFFF;
@@ -272,7 +269,7 @@ __device__ void list_experts(const MxFewArgs &a, const FewWs &ws, const int *id,
   }
   if (tid == kMaxE / 4 - 1) {
     *ws.n_active = ex >> 16;
-    if (GROUPED && a.E == kMaxE) ws.offsets[kMaxE] = ex & 0xFFFF;
+    if (a.E == kMaxE) ws.offsets[kMaxE] = ex & 0xFFFF;
     ws.act_row[ex >> 16] = ex & 0xFFFF;
   }
   __syncthreads();
@@ -281,17 +278,8 @@ __device__ void list_experts(const MxFewArgs &a, const FewWs &ws, const int *id,
     if (e < 0) continue;
     const int t = few_token(f, a.T), r = sh.start[e] + __popcll(sh.mask[e] & ((1ull << t) - 1ull));
     ws.row_f[r] = f;
-    if (GROUPED) ws.row_token[r] = t;
+    ws.row_token[r] = t;
   }
-}
-
-// few_grouped: the rows' order, for the grouped GEMM that takes k_few_gate_up's place
-__global__ __launch_bounds__(kGuThreads) void k_few_group(MxFewArgs a) {
-  FewWs ws;
-  few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
-  __shared__ FewList list;
-  for (int i = threadIdx.x; i < (a.H + 15) / 16; i += kGuThreads) ws.arrived[i] = 0;
-  list_experts<true>(a, ws, ws.id, list);
 }
 
 // FUSED (logits given, T <= kFusedTokens, T * H <= kFusedElems): routes and quantises x as well;
@@ -300,11 +288,7 @@ template <bool FUSED, int NPL, int LPT, bool F32>
 __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
-  union Shared {
-    float part[kGuWaves][16][64];
-    FewList list;
-  };
-  __shared__ Shared sh;
+  __shared__ float part[kGuWaves][16][64];
   __shared__ int rows[kGuWaves][kMaxT];  // one list per wave: no barrier between finding and using it
   __shared__ int s_id[FUSED ? kFusedTokens * 32 : 1];
   __shared__ float s_w[FUSED ? kFusedTokens * 32 : 1];
@@ -358,37 +342,31 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
     __syncthreads();
     id = s_id;
   }
-  if (blockIdx.x == 0) {
-    if constexpr (FUSED) {
-      for (int f = tid; f < R; f += kGuThreads) {
-        ws.id[f] = s_id[f];
-        ws.w[f] = s_w[f];
-      }
+  if (FUSED && blockIdx.x == 0) {
+    for (int f = tid; f < R; f += kGuThreads) {
+      ws.id[f] = s_id[f];
+      ws.w[f] = s_w[f];
     }
     for (int i = tid; i < (a.H + 15) / 16; i += kGuThreads) ws.arrived[i] = 0;
-    if (!few_direct(a)) list_experts<false>(a, ws, id, sh.list);
-    return;
   }
   const int tiles = a.I / 32;
-  const int y = (int)(blockIdx.x - 1) / tiles, c0 = ((int)(blockIdx.x - 1) - y * tiles) * 32;
+  const int y = (int)blockIdx.x / tiles, c0 = ((int)blockIdx.x - y * tiles) * 32;
   // y counts assignments or, when there are fewer of them, experts
   const bool by_f = R <= a.E;
   const int e = by_f ? __builtin_amdgcn_readfirstlane(id[y]) : y;
   if (e < 0) return;
   int n = 0, owner = -1;
-  for (int f0 = 0; f0 < R; f0 += 512) {
-    int ids[8];  // all under way at once
+  int ids[kIdChunks];  // all under way at once
 #pragma unroll
-    for (int c = 0; c < 8; ++c) ids[c] = id[std::min(f0 + c * 64 + lane, R - 1)];
+  for (int c = 0; c < kIdChunks; ++c) ids[c] = id[std::min(c * 64 + lane, R - 1)];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int f = f0 + c * 64 + lane;
-      const bool hit = f < R && ids[c] == e;
-      const unsigned long long m = __ballot(hit);
-      if (hit) rows[wave][n + __popcll(m & ((1ull << lane) - 1ull))] = f;
-      if (m && owner < 0) owner = f0 + c * 64 + __builtin_ctzll(m);
-      n += __popcll(m);
-    }
+  for (int c = 0; c < kIdChunks; ++c) {
+    const int f = c * 64 + lane;
+    const bool hit = f < R && ids[c] == e;
+    const unsigned long long m = __ballot(hit);
+    if (hit) rows[wave][n + __popcll(m & ((1ull << lane) - 1ull))] = f;
+    if (m && owner < 0) owner = c * 64 + __builtin_ctzll(m);
+    n += __popcll(m);
   }
   n = __builtin_amdgcn_readfirstlane(n);
   // nobody's expert, or an earlier assignment's workgroup has it
@@ -427,6 +405,8 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
       if (c > 0 || (q > 0 && steps > chunk)) load_w(s0);  // otherwise the registers hold it
       u32x4 xc[kGuSteps];
       uint32_t xs[kGuSteps];
+      u32x2 xs2 = {0, 0};
+      if constexpr (!FUSED) xs2 = load_scales2(x, tok, s0 * 4);
 #pragma unroll
       for (int i = 0; i < kGuSteps; ++i) {
         const int b = (s0 + i) * 4 + g;
@@ -436,7 +416,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
           xs[i] = live ? s_xs[tok * steps + s0 + i] >> (8 * g) : 0u;
         } else {
           xc[i] = load_codes(x, i < per ? tok : -1, b);
-          xs[i] = load_scale(x, i < per ? tok : -1, b);
+          xs[i] = scale_of(xs2[i], g, i < per ? b : x.nb, x.nb);
         }
       }
 #pragma unroll
@@ -452,7 +432,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sh.part[wave][t * 4 + r][lane] = acc[t][r];
+      for (int r = 0; r < 4; ++r) part[wave][t * 4 + r][lane] = acc[t][r];
     __syncthreads();
     if (tid < 256) {
       // column c sits in tile c / 16, lane (c % 16) / 4 * 16 + slot, register c % 4
@@ -463,8 +443,8 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
         float gate = 0, up = 0;
 #pragma unroll
         for (int v = 0; v < kGuWaves; ++v) {
-          gate += sh.part[v][reg][at];
-          up += sh.part[v][reg + 8][at];
+          gate += part[v][reg][at];
+          up += part[v][reg + 8][at];
         }
         h[u] = gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
       }
@@ -490,15 +470,15 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
 constexpr int kDnWaves = 16, kDnSteps = 6;
 
 // Workgroup (column tile, split): the tile's entries (experts in use, or assignments) are dealt to
-// the waves of its `splits` workgroups in turn.  Of an entry a wave takes the steps part,
-// part + parts, .. (parts > 1 with fewer than 16 entries).  The row numbers of the next entry are
+// the waves of its `splits` workgroups in turn.  Of an entry a wave takes a
+// `parts`-th of the steps (parts > 1 with at most eight entries).  The row numbers of the next entry are
 // loaded while this one is computed.  (Its weights too would take the kernel over 128 registers,
 // that is, to half the waves.)
 // With several splits each workgroup leaves its sums in the workspace, and the last one to
 // arrive adds them up, in split order whoever it is.
 // The SwiGLU rows are in assignment order, or (grouped) in expert order.
-template <bool OUT_F32>
-__global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int splits, int grouped) {
+template <bool OUT_F32, bool GROUPED>
+__global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int splits) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
   extern __shared__ float table[];  // [wave][token][16 columns]
@@ -506,12 +486,12 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int R = a.T * a.k;
-  const bool direct = !grouped && few_direct(a);
-  const int na = direct ? R : __builtin_amdgcn_readfirstlane(*ws.n_active);
+  const int na = GROUPED ? __builtin_amdgcn_readfirstlane(*ws.n_active) : R;
   const int parts = na > 8 || splits > 1 ? 1 : na > 4 ? 2 : 4;
   const int tile = blockIdx.x / splits, split = blockIdx.x - tile * splits;
   const int part = wave % parts, stride = splits * kDnWaves / parts;
   const int steps = (a.I + 127) / 128;
+  const int per = min(kDnSteps, (steps + parts - 1) / parts);  // consecutive steps of a wave
   const int c0 = tile * 16;
   const int wrow = c0 + l < a.H ? c0 + l : -1;
   const Mat h = matrix(ws.h_codes, ws.h_scales, 0, R, a.I);
@@ -520,7 +500,7 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   int le = -1, lr = 0, ln = 0;
   const int i0 = (split * kDnWaves + wave) / parts + lane * stride;
   if (i0 < na) {
-    if (direct) {
+    if (!GROUPED) {
       le = ws.id[i0];
       lr = i0;
       ln = le < 0 ? 0 : 1;
@@ -532,23 +512,29 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   }
   const int count = __popcll(__ballot(i0 < na));
   for (int i = lane; i < a.T * 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
-  const auto load_w = [&](u32x4 (&wc)[kDnSteps], uint32_t (&wsc)[kDnSteps], int e, int s0) __attribute__((always_inline)) {
-    const Mat w2 = matrix(a.w2_codes, a.w2_scales, (int64_t)max(e, 0) * a.H, a.H, a.I);
+  // the wave's steps from s0 on of a row: codes of block g of each, and the scale bytes of all four
+  static_assert(kDnSteps == 6, "six dwords of scale bytes");
+  const auto load = [&](u32x4 (&c)[kDnSteps], uint32_t (&sc)[kDnSteps], const Mat &m, int row, int s0)
+      __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < kDnSteps; ++s) {
-      wc[s] = load_codes(w2, e < 0 ? -1 : wrow, (s0 + s * parts) * 4 + g);
-      wsc[s] = load_scale(w2, e < 0 ? -1 : wrow, (s0 + s * parts) * 4 + g);
-    }
+    for (int s = 0; s < kDnSteps; ++s) c[s] = load_codes(m, s < per ? row : -1, (s0 + s) * 4 + g);
+    const uint32_t at = row >= 0 && s0 < steps ? (uint32_t)(row * m.sld + s0 * 4) : kOut;
+    const u32x4 lo = load16(m.scales, m.sbytes, at);
+    const u32x2 hi = load8(m.scales, m.sbytes, per > 4 ? at + 16 : kOut);
+    sc[0] = lo[0], sc[1] = lo[1], sc[2] = lo[2], sc[3] = lo[3], sc[4] = hi[0], sc[5] = hi[1];
+  };
+  const auto load_w = [&](u32x4 (&wc)[kDnSteps], uint32_t (&wsc)[kDnSteps], int e, int s0) __attribute__((always_inline)) {
+    load(wc, wsc, matrix(a.w2_codes, a.w2_scales, (int64_t)max(e, 0) * a.H, a.H, a.I), e < 0 ? -1 : wrow, s0);
   };
   const auto row_of = [&](int r0, int n, int q) __attribute__((always_inline)) {  // assignment of row slot q + l, or -1
-    return q + l < n ? (direct ? r0 : ws.row_f[r0 + q + l]) : -1;
+    return q + l < n ? (GROUPED ? ws.row_f[r0 + q + l] : r0) : -1;
   };
   u32x4 w[kDnSteps];
   uint32_t wsc[kDnSteps];
   int e = __builtin_amdgcn_readlane(le, 0), r0 = __builtin_amdgcn_readlane(lr, 0), n = __builtin_amdgcn_readlane(ln, 0);
-  load_w(w, wsc, e, part);
+  load_w(w, wsc, e, part * per);
   int f = row_of(r0, n, 0);
-  const bool once = steps <= parts * kDnSteps;  // the registers hold the whole row
+  const bool once = steps <= parts * per;  // the registers hold the whole row
   for (int c = 0; c < count; ++c) {
     const int c1 = min(c + 1, 63);
     const bool more = c + 1 < count;
@@ -558,19 +544,18 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
     for (int q = 0; q < n; q += 16) {
       if (q > 0) f = row_of(r0, n, q);
       const float wt = f >= 0 ? ws.w[f] : 0.0f;
-      const int hr = !grouped ? f : q + l < n ? r0 + q + l : -1;
+      const int hr = !GROUPED ? f : q + l < n ? r0 + q + l : -1;
       f32x4 acc = f32x4{0, 0, 0, 0};
-      for (int s0 = part; s0 < steps; s0 += parts * kDnSteps) {
-        if (!once && (s0 != part || q > 0)) load_w(w, wsc, e, s0);
+      for (int s0 = part * per; s0 < steps; s0 += parts * per) {
+        if (!once && (s0 != part * per || q > 0)) load_w(w, wsc, e, s0);
         u32x4 x[kDnSteps];
         uint32_t xs[kDnSteps];
+        load(x, xs, h, hr, s0);
 #pragma unroll
         for (int s = 0; s < kDnSteps; ++s) {
-          x[s] = load_codes(h, hr, (s0 + s * parts) * 4 + g);
-          xs[s] = load_scale(h, hr, (s0 + s * parts) * 4 + g);
+          const int b = s < per ? (s0 + s) * 4 + g : h.nb;
+          acc = mfma16(w[s], scale_of(wsc[s], g, b, h.nb), x[s], scale_of(xs[s], g, b, h.nb), acc);
         }
-#pragma unroll
-        for (int s = 0; s < kDnSteps; ++s) acc = mfma16(w[s], wsc[s], x[s], xs[s], acc);
       }
       // lane = row slot l, columns 4 g ..: an expert's rows are different tokens, so no two
       // lanes meet in the table
@@ -588,7 +573,7 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
     r0 = r1;
     n = n1;
     f = f1;
-    if (more) load_w(w, wsc, e, part);
+    if (more) load_w(w, wsc, e, part * per);
   }
   __syncthreads();
   const auto store = [&](int i, float v) __attribute__((always_inline)) {
@@ -624,8 +609,6 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   }
 }
 
-// Batches with more assignments than this go through the grouped GEMM (see the top).
-constexpr int kGroupedRows = 72;
 bool few_grouped(const MxFewArgs &a) { return a.T * a.k > kGroupedRows; }
 
 // The smallest batches: one kernel less (see the top).
@@ -635,7 +618,7 @@ bool few_fused(const MxFewArgs &a) {
 
 template <int NPL, int LPT, bool F32>
 hipError_t launch_first(const MxFewArgs &a, hipStream_t stream) {
-  const unsigned grid = 1 + (unsigned)(a.I / 32) * (unsigned)std::min(a.E, a.T * a.k);  // experts in use
+  const unsigned grid = (unsigned)(a.I / 32) * (unsigned)std::min(a.E, a.T * a.k);  // experts in use
   if (few_fused(a)) {
     k_few_gate_up<true, NPL, LPT, F32><<<grid, kGuThreads, 0, stream>>>(a);
     return hipSuccess;
@@ -696,8 +679,10 @@ hipError_t launch_mx_few(const MxFewArgs &a, hipStream_t stream) {
   // workgroups for the whole chip, at least an entry for each of their waves
   const int splits = std::max(1, std::min({kMaxSplits, device_cu_count() / tiles, entries / kDnWaves}));
   const unsigned grid = (unsigned)(tiles * splits);
-  if (a.out_is_f32) k_few_down<true><<<grid, kDnWaves * 64, lds, stream>>>(a, splits, few_grouped(a));
-  else k_few_down<false><<<grid, kDnWaves * 64, lds, stream>>>(a, splits, few_grouped(a));
+  const bool grouped = few_grouped(a);
+  const auto kernel = a.out_is_f32 ? (grouped ? k_few_down<true, true> : k_few_down<true, false>)
+                                   : (grouped ? k_few_down<false, true> : k_few_down<false, false>);
+  kernel<<<grid, kDnWaves * 64, lds, stream>>>(a, splits);
   return hipGetLastError();
 }
 
