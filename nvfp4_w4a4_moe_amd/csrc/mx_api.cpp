@@ -167,10 +167,11 @@ nv4_status mxfp4_grouped_gemm(const nv4_mx_tensor *A, const nv4_mx_tensor *B, co
   if (A->K == 0) return fail(NV4_EINVAL, "%s: K must be positive", fn);
   const int64_t esz = ctype == NV4_F32 ? 4 : 2;
   if (!aligned(C, esz)) return fail(NV4_EALIGN, "%s: C is not aligned to its type", fn);
-  // byte offsets into an operand are 32-bit, and one below 2^32 - 256 marks an absent row
+  // byte offsets into A and into an expert's part of B are 32-bit; one below 2^32 - 256 marks an
+  // absent row
   const int64_t most = 0xFFFFFF00ll;
-  if (A->rows * (A->K / 2) > most || B->rows * (B->K / 2) > most)
-    return fail(NV4_EINVAL, "%s: each operand must stay below 4 GiB of codes", fn);
+  if (A->rows * (A->K / 2) > most || (group_mode == NV4_GROUP_K ? B->rows : B->rows / E) * (B->K / 2) > most)
+    return fail(NV4_EINVAL, "%s: A and an expert's part of B must each stay below 4 GiB of codes", fn);
   const int64_t ncols = group_mode == NV4_GROUP_K ? B->rows : N;
   if (C && ldc < ncols) return fail(NV4_EINVAL, "%s: ldc < columns of C", fn);
   // columns and tiles are counted in 32 bits, a tile's rows of C addressed with 32-bit offsets

@@ -64,4 +64,33 @@ __device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
                             __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
 }
 
+// Loads straight into LDS: lane i of the wave brings 16 (4) bytes at byte offset voff to
+// dst + 16 i (4 i); an offset behind the buffer brings zeros.
+typedef __attribute__((address_space(3))) void *mx_lds_ptr;
+__device__ __forceinline__ void mx_dma16(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst,
+      16, voff, 0, 0, 0);
+}
+__device__ __forceinline__ void mx_dma4(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 4,
+      voff, 0, 0, 0);
+}
+
+// wait until at most N vector-memory operations of this wave are outstanding
+template <int N>
+__device__ __forceinline__ void mx_wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+// wait for this wave's LDS operations (lgkmcnt(0) only)
+__device__ __forceinline__ void mx_wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace nv4

@@ -26,6 +26,7 @@
 // bytes.  Loads are buffer loads, whose offsets behind the row's end or without a row give
 // zeros without a branch.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.h"
 #include "mx_internal.h"
@@ -48,8 +49,9 @@ constexpr uint32_t kOut = 0xFFFFFF00u;  // a byte offset behind every buffer
 struct FewWs {
   int32_t *id;
   float *w;
-  int32_t *n_active, *act_e, *act_row, *row_f;
-  int32_t *offsets, *row_token;  // few_grouped: every expert's first row, the rows' tokens
+  int32_t *n_active, *act_e, *act_row;
+  int32_t *offsets, *row_token;  // every expert's first row, the rows' tokens and weights
+  float *row_w;
   int32_t *arrived;  // per column tile of the down product: workgroups that left their sums
   float *sums;       // [tile][split][token][16]
   uint8_t *x_codes, *x_scales, *h_codes, *h_scales;
@@ -70,7 +72,7 @@ __host__ __device__ inline size_t few_ws(void *base, int64_t T, int E, int k, in
   w.n_active = reinterpret_cast<int32_t *>(take(4));
   w.act_e = reinterpret_cast<int32_t *>(take(A * 4));
   w.act_row = reinterpret_cast<int32_t *>(take((A + 1) * 4));
-  w.row_f = reinterpret_cast<int32_t *>(take(R * 4));
+  w.row_w = reinterpret_cast<float *>(take(R * 4));
   w.offsets = reinterpret_cast<int32_t *>(take((E + 1) * 4));
   w.row_token = reinterpret_cast<int32_t *>(take(R * 4));
   const int64_t tiles = (H + 15) / 16;
@@ -192,7 +194,7 @@ __device__ __forceinline__ Mat matrix(const uint8_t *codes, const uint8_t *scale
 }
 // Block b of a row (row < 0: none): its 32 codes; zeros behind K.
 __device__ __forceinline__ u32x4 load_codes(const Mat &m, int row, int b) {
-  return load16(m.codes, m.cbytes, row >= 0 && b < m.nb ? (uint32_t)(row * m.nb + b) * 16u : kOut);
+  return load16(m.codes, m.cbytes, ((row >= 0) & (b < m.nb)) ? (uint32_t)(row * m.nb + b) * 16u : kOut);
 }
 // The scale bytes of two consecutive steps (8 blocks from block b0, a multiple of 4) of a row:
 // dword i holds step i's four blocks, of which lane group g takes byte g (and b0 + 4 i + g < nb).
@@ -212,6 +214,7 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t 
 
 constexpr int kGuWaves = 8, kGuSteps = 2;  // steps of K = 128 a wave holds at a time
 constexpr int kGuThreads = kGuWaves * 64;
+constexpr int kGuCodes = 64 * kGuSteps * 64, kGuSlot = kGuCodes + 64 * kGuSteps * 4;
 
 // Batches with more assignments than this go through the grouped GEMM (see the top).
 constexpr int kGroupedRows = 72;
@@ -277,7 +280,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_group(MxFewArgs a) {
     const int e = id[f];
     if (e < 0) continue;
     const int t = few_token(f, a.T), r = sh.start[e] + __popcll(sh.mask[e] & ((1ull << t) - 1ull));
-    ws.row_f[r] = f;
+    ws.row_w[r] = ws.w[f];
     ws.row_token[r] = t;
   }
 }
@@ -288,7 +291,11 @@ template <bool FUSED, int NPL, int LPT, bool F32>
 __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
-  __shared__ float part[kGuWaves][16][64];
+  // a wave's part of W13: 64 rows of kGuSteps steps, and their scale bytes; afterwards its sums
+  __shared__ __attribute__((aligned(1024))) uint8_t slots[kGuWaves * kGuSlot];
+  const auto part = [&](int v, int reg) __attribute__((always_inline)) {
+    return reinterpret_cast<float *>(slots + v * kGuSlot) + reg * 64;
+  };
   __shared__ int rows[kGuWaves][kMaxT];  // one list per wave: no barrier between finding and using it
   __shared__ int s_id[FUSED ? kFusedTokens * 32 : 1];
   __shared__ float s_w[FUSED ? kFusedTokens * 32 : 1];
@@ -376,17 +383,24 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
   const Mat x = matrix(ws.x_codes, ws.x_scales, 0, a.T, a.H);
   const int per = min(kGuSteps, (steps + kGuWaves - 1) / kGuWaves);  // consecutive steps of a wave
   const int chunk = per * kGuWaves;
-  // tiles: gate columns c0.., c0 + 16.., then the up rows
-  static_assert(kGuSteps == 2, "load_scales2");
-  u32x4 w[kGuSteps][4];
-  u32x2 wsc[4];
+  static_assert(kGuSteps == 2, "128 bytes of codes and two dwords of scale bytes a row");
+  // LDS position 16 p of the codes (p = 64 i + lane) holds block (p % 8) ^ (row / 2 % 8) of row p / 8:
+  // the 16 rows of one read then lie in different banks
+  uint8_t *mine = slots + wave * kGuSlot;
   const auto load_w = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int row = c0 + (t & 1) * 16 + (t >> 1) * a.I + l;
+    for (int i = 0; i < kGuCodes / 1024; ++i) {
+      const int r = i * 8 + (lane >> 3), b = (lane & 7) ^ ((r >> 1) & 7);
+      const int row = c0 + (r & 31) + (r >> 5) * a.I;
+      const bool in = (b < per * 4) & (s0 * 4 + b < w13.nb);
+      mx_dma16(w13.codes, w13.cbytes, mine + i * 1024, in ? (uint32_t)(row * w13.nb + s0 * 4 + b) * 16u : kOut);
+    }
 #pragma unroll
-      for (int i = 0; i < kGuSteps; ++i) w[i][t] = load_codes(w13, i < per ? row : -1, (s0 + i) * 4 + g);
-      wsc[t] = load_scales2(w13, row, s0 * 4);
+    for (int j = 0; j < 2; ++j) {
+      const int r = j * 32 + (lane >> 1), d = lane & 1;
+      const int row = c0 + (r & 31) + (r >> 5) * a.I;
+      const bool in = (d < per) & (s0 + d < steps);
+      mx_dma4(w13.scales, w13.sbytes, mine + kGuCodes + j * 256, in ? (uint32_t)(row * w13.sld + (s0 + d) * 4) : kOut);
     }
   };
   load_w(wave * per);
@@ -396,13 +410,17 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   for (int q = 0; q < n; q += 16) {
+    if (q) {
+      __syncthreads();  // the sums of the rows before have been read
+      load_w(wave * per);
+    }
     const int tok = q + l < n ? few_token(rows[wave][q + l], a.T) : -1;
     f32x4 acc[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
     for (int c = 0; c < steps; c += chunk) {
       const int s0 = c + wave * per;
-      if (c > 0 || (q > 0 && steps > chunk)) load_w(s0);  // otherwise the registers hold it
+      if (c > 0) load_w(s0);
       u32x4 xc[kGuSteps];
       uint32_t xs[kGuSteps];
       u32x2 xs2 = {0, 0};
@@ -419,20 +437,25 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
           xs[i] = scale_of(xs2[i], g, i < per ? b : x.nb, x.nb);
         }
       }
+      mx_wait_vm<0>();
 #pragma unroll
-      for (int i = 0; i < kGuSteps; ++i) {
-        const int b = (s0 + i) * 4 + g;
+      for (int t = 0; t < 4; ++t) {
+        const int r = t * 16 + l;  // gate columns c0.., c0 + 16.., then the up rows
+        const u32x2 wsc = *reinterpret_cast<const u32x2 *>(mine + kGuCodes + r * 8);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          acc[t] = mfma16(w[i][t], scale_of(wsc[t][i], g, i < per ? b : x.nb, x.nb), xc[i], xs[i], acc[t]);
+        for (int i = 0; i < kGuSteps; ++i) {
+          const int b = (s0 + i) * 4 + g;
+          const u32x4 w = *reinterpret_cast<const u32x4 *>(mine + (r * 8 + ((i * 4 + g) ^ ((r >> 1) & 7))) * 16);
+          acc[t] = mfma16(w, scale_of(wsc[i], g, i < per ? b : w13.nb, w13.nb), xc[i], xs[i], acc[t]);
+        }
       }
+      mx_wait_lds();  // the next steps or the sums take the place
     }
     // sum over the waves, SwiGLU, re-quantise: thread = token slot of 16, two columns
-    if (q) __syncthreads();
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave][t * 4 + r][lane] = acc[t][r];
+      for (int r = 0; r < 4; ++r) part(wave, t * 4 + r)[lane] = acc[t][r];
     __syncthreads();
     if (tid < 256) {
       // column c sits in tile c / 16, lane (c % 16) / 4 * 16 + slot, register c % 4
@@ -443,8 +466,8 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
         float gate = 0, up = 0;
 #pragma unroll
         for (int v = 0; v < kGuWaves; ++v) {
-          gate += part[v][reg][at];
-          up += part[v][reg + 8][at];
+          gate += part(v, reg)[at];
+          up += part(v, reg + 8)[at];
         }
         h[u] = gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
       }
@@ -467,13 +490,17 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
 
 // ---------------------------------------------------------------- 3. down
 
-constexpr int kDnWaves = 16, kDnSteps = 6;
+constexpr int kDnWaves = 8, kDnSteps = 6;
+constexpr int kDnCodes = 16 * kDnSteps * 64;  // 16 rows of a window of kDnSteps steps
+constexpr int kDnSlot = kDnCodes + 512;       // and their scale bytes, kDnSteps dwords a row
+constexpr int kDnDma = kDnCodes / 1024 + 2;
 
 // Workgroup (column tile, split): the tile's entries (experts in use, or assignments) are dealt to
-// the waves of its `splits` workgroups in turn.  Of an entry a wave takes a
-// `parts`-th of the steps (parts > 1 with at most eight entries).  The row numbers of the next entry are
-// loaded while this one is computed.  (Its weights too would take the kernel over 128 registers,
-// that is, to half the waves.)
+// the waves of its `splits` workgroups in turn, each in windows of up to kDnSteps steps.  Of an
+// entry a wave takes a `parts`-th of the steps (parts > 1 with at most four entries).
+// W2's 16 rows of a window go straight to the wave's own part of LDS, the next window's while
+// this one is computed, with no barrier.  Taken to registers in the products' layout they cost
+// the address unit one access a lane, since 16 adjacent lanes hold 16 rows: XX.
 // With several splits each workgroup leaves its sums in the workspace, and the last one to
 // arrive adds them up, in split order whoever it is.
 // The SwiGLU rows are in assignment order, or (grouped) in expert order.
@@ -482,24 +509,27 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   FewWs ws;
   few_ws(a.ws, a.T, a.E, a.k, a.H, a.I, ws);
   extern __shared__ float table[];  // [wave][token][16 columns]
+  // (two arrays: the compiler then knows that reads of one do not depend on the loads into the other)
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[kDnWaves * kDnSlot], ring1[kDnWaves * kDnSlot];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int R = a.T * a.k;
-  const int na = GROUPED ? __builtin_amdgcn_readfirstlane(*ws.n_active) : R;
-  const int parts = na > 8 || splits > 1 ? 1 : na > 4 ? 2 : 4;
+  const int most = min(a.E, R);  // entries
+  const int parts = most > 4 || splits > 1 ? 1 : most > 2 ? 2 : 4;
   const int tile = blockIdx.x / splits, split = blockIdx.x - tile * splits;
   const int part = wave % parts, stride = splits * kDnWaves / parts;
   const int steps = (a.I + 127) / 128;
-  const int per = min(kDnSteps, (steps + parts - 1) / parts);  // consecutive steps of a wave
+  const int per = min(kDnSteps, (steps + parts - 1) / parts);  // consecutive steps of a wave's window
+  const int windows = (steps + parts * per - 1) / (parts * per);
   const int c0 = tile * 16;
-  const int wrow = c0 + l < a.H ? c0 + l : -1;
   const Mat h = matrix(ws.h_codes, ws.h_scales, 0, R, a.I);
   float *mine = table + wave * a.T * 16;
   // the wave's entries, one per lane (at most 1024 / 16 of them): expert, first row, rows
   int le = -1, lr = 0, ln = 0;
   const int i0 = (split * kDnWaves + wave) / parts + lane * stride;
-  if (i0 < na) {
+  const int na = GROUPED ? *ws.n_active : R;  // (arrives with the entries, not before them)
+  if (i0 < (GROUPED ? most : R)) {
     if (!GROUPED) {
       le = ws.id[i0];
       lr = i0;
@@ -510,71 +540,116 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
       ln = ws.act_row[i0 + 1] - lr;
     }
   }
-  const int count = __popcll(__ballot(i0 < na));
+  const int count = __popcll(__ballot(i0 < na)) * windows;
+  if (i0 >= na) le = -1, ln = 0;
   for (int i = lane; i < a.T * 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
-  // the wave's steps from s0 on of a row: codes of block g of each, and the scale bytes of all four
-  static_assert(kDnSteps == 6, "six dwords of scale bytes");
-  const auto load = [&](u32x4 (&c)[kDnSteps], uint32_t (&sc)[kDnSteps], const Mat &m, int row, int s0)
-      __attribute__((always_inline)) {
+  // LDS position 16 p (p = 64 i + lane) holds block (p % 24) ^ (row / 2 % 8) of row p / 24: the 16
+  // rows' same block then lies in 16 different groups of banks
+  constexpr int kRow = kDnSteps * 4;
+  int at_row[kDnCodes / 1024], at_b[kDnCodes / 1024];
 #pragma unroll
-    for (int s = 0; s < kDnSteps; ++s) c[s] = load_codes(m, s < per ? row : -1, (s0 + s) * 4 + g);
-    const uint32_t at = row >= 0 && s0 < steps ? (uint32_t)(row * m.sld + s0 * 4) : kOut;
-    const u32x4 lo = load16(m.scales, m.sbytes, at);
-    const u32x2 hi = load8(m.scales, m.sbytes, per > 4 ? at + 16 : kOut);
-    sc[0] = lo[0], sc[1] = lo[1], sc[2] = lo[2], sc[3] = lo[3], sc[4] = hi[0], sc[5] = hi[1];
+  for (int i = 0; i < kDnCodes / 1024; ++i) {
+    const int p = i * 64 + lane, r = p / kRow;
+    at_row[i] = c0 + r < a.H ? r : -1;
+    at_b[i] = (p - r * kRow) ^ ((r >> 1) & 7);
+  }
+  struct Item {
+    int e, r0, n, s0;
   };
-  const auto load_w = [&](u32x4 (&wc)[kDnSteps], uint32_t (&wsc)[kDnSteps], int e, int s0) __attribute__((always_inline)) {
-    load(wc, wsc, matrix(a.w2_codes, a.w2_scales, (int64_t)max(e, 0) * a.H, a.H, a.I), e < 0 ? -1 : wrow, s0);
+  // item c: entry c / windows, window c % windows (counted up alongside, ic and iw)
+  int ic = 0, iw = 0;
+  const auto next_item = [&]() __attribute__((always_inline)) -> Item {
+    const Item it{__builtin_amdgcn_readlane(le, ic), __builtin_amdgcn_readlane(lr, ic),
+                  __builtin_amdgcn_readlane(ln, ic), (iw * parts + part) * per};
+    if (++iw == windows) iw = 0, ++ic;
+    return it;
   };
-  const auto row_of = [&](int r0, int n, int q) __attribute__((always_inline)) {  // assignment of row slot q + l, or -1
-    return q + l < n ? (GROUPED ? ws.row_f[r0 + q + l] : r0) : -1;
+  const auto dma = [&](uint8_t *ring, const Item &it) __attribute__((always_inline)) {
+    const Mat w2 = matrix(a.w2_codes, a.w2_scales, (int64_t)max(it.e, 0) * a.H + c0, min(16, a.H - c0), a.I);
+    uint8_t *dst = ring + wave * kDnSlot;
+    const bool live = it.e >= 0;
+#pragma unroll
+    for (int i = 0; i < kDnCodes / 1024; ++i) {
+      const int b = it.s0 * 4 + at_b[i];
+      const bool in = live & (at_row[i] >= 0) & (at_b[i] < per * 4) & (b < w2.nb);
+      mx_dma16(w2.codes, w2.cbytes, dst + i * 1024, in ? (uint32_t)(at_row[i] * w2.nb + b) * 16u : kOut);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int p = j * 64 + lane, r = p / kDnSteps, d = p - r * kDnSteps;
+      const bool in = live & (r < 16) & (c0 + r < a.H) & (d < per) & (it.s0 + d < steps);
+      mx_dma4(w2.scales, w2.sbytes, dst + kDnCodes + j * 256,
+              in ? (uint32_t)(r * w2.sld + (it.s0 + d) * 4) : kOut);
+    }
   };
-  u32x4 w[kDnSteps];
-  uint32_t wsc[kDnSteps];
-  int e = __builtin_amdgcn_readlane(le, 0), r0 = __builtin_amdgcn_readlane(lr, 0), n = __builtin_amdgcn_readlane(ln, 0);
-  load_w(w, wsc, e, part * per);
-  int f = row_of(r0, n, 0);
-  const bool once = steps <= parts * per;  // the registers hold the whole row
-  for (int c = 0; c < count; ++c) {
-    const int c1 = min(c + 1, 63);
+  // rows q .. q + 15 of an entry: row slot l's steps from s0 on, weight and token
+  struct Rows {
+    u32x4 c[kDnSteps];
+    u32x4 lo;
+    u32x2 hi;
+    float w;
+    int t;
+  };
+  const auto load_rows = [&](Rows &x, const Item &it, int q) __attribute__((always_inline)) {
+    const int row = q + l < it.n ? it.r0 + q + l : -1;
+#pragma unroll
+    for (int s = 0; s < kDnSteps; ++s) x.c[s] = load_codes(h, s < per ? row : -1, (it.s0 + s) * 4 + g);
+    const uint32_t at = ((row >= 0) & (it.s0 < steps)) ? (uint32_t)(row * h.sld + it.s0 * 4) : kOut;
+    x.lo = load16(h.scales, h.sbytes, at);
+    x.hi = load8(h.scales, h.sbytes, per > 4 ? at + 16 : kOut);
+    x.w = (GROUPED ? ws.row_w : ws.w)[max(row, 0)];
+    x.t = GROUPED ? ws.row_token[max(row, 0)] : few_token(max(row, 0), a.T);
+  };
+  Item it = count > 0 ? next_item() : Item{-1, 0, 0, 0};
+  Rows x[2];
+  dma(ring0, it);
+  load_rows(x[0], it, 0);
+  const auto item = [&](auto P, int c) __attribute__((always_inline)) {
+    constexpr int p = decltype(P)::value;
     const bool more = c + 1 < count;
-    const int e1 = more ? __builtin_amdgcn_readlane(le, c1) : -1, r1 = __builtin_amdgcn_readlane(lr, c1);
-    const int n1 = more ? __builtin_amdgcn_readlane(ln, c1) : 0;
-    const int f1 = row_of(r1, n1, 0);
-    for (int q = 0; q < n; q += 16) {
-      if (q > 0) f = row_of(r0, n, q);
-      const float wt = f >= 0 ? ws.w[f] : 0.0f;
-      const int hr = !GROUPED ? f : q + l < n ? r0 + q + l : -1;
+    const Item cur = it;
+    // W2's window and the rows of this item were asked for before the next window
+    if (more) {
+      it = next_item();
+      dma(p ? ring0 : ring1, it);
+      mx_wait_vm<kDnDma>();
+      load_rows(x[1 - p], it, 0);
+    } else {
+      mx_wait_vm<0>();
+    }
+    const uint8_t *w = (p ? ring1 : ring0) + wave * kDnSlot;
+    for (int q = 0; q < cur.n; q += 16) {
+      if (q > 0) load_rows(x[p], cur, q);
+      const uint32_t xs[kDnSteps] = {x[p].lo[0], x[p].lo[1], x[p].lo[2], x[p].lo[3], x[p].hi[0], x[p].hi[1]};
       f32x4 acc = f32x4{0, 0, 0, 0};
-      for (int s0 = part * per; s0 < steps; s0 += parts * per) {
-        if (!once && (s0 != part * per || q > 0)) load_w(w, wsc, e, s0);
-        u32x4 x[kDnSteps];
-        uint32_t xs[kDnSteps];
-        load(x, xs, h, hr, s0);
 #pragma unroll
-        for (int s = 0; s < kDnSteps; ++s) {
-          const int b = s < per ? (s0 + s) * 4 + g : h.nb;
-          acc = mfma16(w[s], scale_of(wsc[s], g, b, h.nb), x[s], scale_of(xs[s], g, b, h.nb), acc);
-        }
+      for (int s = 0; s < kDnSteps; ++s) {
+        const int b = s < per ? (cur.s0 + s) * 4 + g : h.nb;
+        const u32x4 wc = *reinterpret_cast<const u32x4 *>(w + (l * kRow + ((s * 4 + g) ^ ((l >> 1) & 7))) * 16);
+        const uint32_t wsc = *reinterpret_cast<const uint32_t *>(w + kDnCodes + (l * kDnSteps + s) * 4);
+        acc = mfma16(wc, scale_of(wsc, g, b, h.nb), x[p].c[s], scale_of(xs[s], g, b, h.nb), acc);
       }
+      // The products of all lanes: without this the compiler moves them, and the scales that they
+      // take from every lane, under the condition below.
+      asm volatile("" : "+v"(acc));
       // lane = row slot l, columns 4 g ..: an expert's rows are different tokens, so no two
       // lanes meet in the table
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      if (f >= 0) {
-        f32x4 *p = reinterpret_cast<f32x4 *>(mine + few_token(f, a.T) * 16 + g * 4);
-        f32x4 v = *p;
+      if (q + l < cur.n) {
+        f32x4 *dst = reinterpret_cast<f32x4 *>(mine + x[p].t * 16 + g * 4);
+        f32x4 v = *dst;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] += wt * acc[u];
-        *p = v;
+        for (int u = 0; u < 4; ++u) v[u] += x[p].w * acc[u];
+        *dst = v;
       }
     }
-    e = e1;
-    r0 = r1;
-    n = n1;
-    f = f1;
-    if (more) load_w(w, wsc, e, part * per);
+  };
+  for (int c = 0; c < count; c += 2) {
+    item(std::integral_constant<int, 0>{}, c);
+    if (c + 1 < count) item(std::integral_constant<int, 1>{}, c + 1);
   }
+  mx_wait_vm<0>();  // loads into this workgroup's LDS end before it does
   __syncthreads();
   const auto store = [&](int i, float v) __attribute__((always_inline)) {
     const int t = i >> 4, c = c0 + (i & 15);

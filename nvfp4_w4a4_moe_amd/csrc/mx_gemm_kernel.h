@@ -86,33 +86,6 @@ __device__ __forceinline__ int mx_swz(int q, int r) {
   return Cfg::kSteps == 2 ? q ^ ((r >> 2) & 3) : q ^ ((r >> 1) & 7);
 }
 
-typedef __attribute__((address_space(3))) void *mx_lds_ptr;
-__device__ __forceinline__ void mx_dma16(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst,
-      16, voff, 0, 0, 0);
-}
-__device__ __forceinline__ void mx_dma4(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 4,
-      voff, 0, 0, 0);
-}
-
-// wait until at most N vector-memory operations of this wave are outstanding
-template <int N>
-__device__ __forceinline__ void mx_wait_vm() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-  asm volatile("" ::: "memory");
-}
-// wait for this wave's LDS operations (lgkmcnt(0) only)
-__device__ __forceinline__ void mx_wait_lds() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);
-  asm volatile("" ::: "memory");
-}
-
 // workgroup barrier without a memory fence (which would drain the prefetches)
 __device__ __forceinline__ void mx_barrier() {
   asm volatile("" ::: "memory");
@@ -256,23 +229,23 @@ struct MxTiles {
   }
 };
 
-// Row of B for tile row r, or -1 behind the matrix.  SwiGLU: a wave's fragments are FN/2 of
+// Row of B (of the tile's expert's part of it) for tile row r, or -1 behind the matrix.  SwiGLU: a wave's fragments are FN/2 of
 // gate rows, then the up rows of the same columns.
 template <class Cfg, int GROUP, int EPI, bool TRANS>
-__device__ __forceinline__ int64_t mx_b_row(const MxGemmArgs &g, const MxJob &j, int r) {
+__device__ __forceinline__ int mx_b_row(const MxGemmArgs &g, const MxJob &j, int r) {
   const int in = TRANS ? (r & ~31) | frag_row(r & 31) : r;
   if (GROUP == NV4_GROUP_K) {
     const int64_t col = (int64_t)j.nt * Cfg::BN + in;
-    return col < g.b_rows ? col : -1;
+    return col < g.b_rows ? (int)col : -1;
   }
   if (EPI == NV4_EPI_SWIGLU) {
     constexpr int half = Cfg::kFN / 2;
     const int wv = in / (Cfg::kFN * 32), f = (in / 32) % Cfg::kFN;
     const int64_t col = (int64_t)j.nt * (Cfg::BN / 2) + wv * (half * 32) + (f % half) * 32 + (in & 31);
-    return col < g.N ? ((int64_t)j.e * 2 + (f >= half ? 1 : 0)) * g.N + col : -1;
+    return col < g.N ? (int)((f >= half ? g.N : 0) + col) : -1;
   }
   const int64_t col = (int64_t)j.nt * Cfg::BN + in;
-  return col < g.N ? (int64_t)j.e * g.N + col : -1;
+  return col < g.N ? (int)col : -1;
 }
 
 template <class Cfg, int GROUP, int EPI, bool OUT_F32, bool TRANS>
@@ -297,7 +270,9 @@ void k_mx_gemm(MxGemmArgs g) {
   const int h = lane >> 5, l32 = lane & 31;
   const int64_t ld = g.K / 2, sld = (g.K / kMxBlock + 3) / 4 * 4;
   const uint32_t a_bytes = (uint32_t)(g.a_rows * ld), a_sbytes = (uint32_t)(g.a_rows * sld);
-  const uint32_t b_bytes = (uint32_t)(g.b_rows * ld), b_sbytes = (uint32_t)(g.b_rows * sld);
+  // B is addressed from the tile's expert, so that only one expert's part must stay below 4 GiB
+  const int64_t b_rows = GROUP == NV4_GROUP_M ? (SWIGLU ? 2 : 1) * g.N : g.b_rows;
+  const uint32_t b_bytes = (uint32_t)(b_rows * ld), b_sbytes = (uint32_t)(b_rows * sld);
 
   // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty)
   for (int e = tid; e <= g.E; e += NT) off[e] = std::max(g.offsets[e], 0);
@@ -371,10 +346,16 @@ void k_mx_gemm(MxGemmArgs g) {
     int row = pj.m0 + (r - BN);
     row = r < BN + BM && row < pj.m_end ? row : -1;
     if (gather && row >= 0) row = min(max(mx_table(idx + lane), 0), (int)g.a_rows - 1);
-    if (Cfg::kOneSide ? wave * Cfg::kWaveCodeRows < BN : r < BN) row = (int)mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
+    if (Cfg::kOneSide ? wave * Cfg::kWaveCodeRows < BN : r < BN) row = mx_b_row<Cfg, GROUP, EPI, TRANS>(g, pj, r);
     return row;
   };
+  const uint8_t *b_codes = g.b_codes, *b_scales = g.b_scales;  // the expert's
   const auto p_setup = [&]() MX_INLINE {
+    if (GROUP == NV4_GROUP_M) {
+      const int64_t first = (int64_t)pj.e * b_rows;
+      b_codes = g.b_codes + first * ld;
+      b_scales = g.b_scales + first * sld;
+    }
     const int mc = p_row(wave * Cfg::kWaveCodeRows + lane, rows_c[wave]);
     const int ms = Cfg::kSameRows ? mc : p_row(wave * Cfg::kWaveScaleRows + lane, rows_s[wave]);
 #pragma unroll
@@ -408,14 +389,14 @@ void k_mx_gemm(MxGemmArgs g) {
       // (saturating: without a row the sum stays behind the buffer)
       const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], kc) : kNoRow;
       const bool isb = b * Cfg::kCodeRows < BN;
-      mx_dma16(isb ? g.b_codes : g.a_codes, isb ? b_bytes : a_bytes, dst + b * 1024, v);
+      mx_dma16(isb ? b_codes : g.a_codes, isb ? b_bytes : a_bytes, dst + b * 1024, v);
     }
 #pragma unroll
     for (int i = 0; i < Cfg::kScaleDma; ++i) {
       const int b = wave * Cfg::kScaleDma + i;
       const uint32_t v = sdw * 128 < left ? __builtin_elementwise_add_sat(off_s[i], ks) : kNoRow;
       const bool isb = b * Cfg::kScaleRows < BN;
-      mx_dma4(isb ? g.b_scales : g.a_scales, isb ? b_sbytes : a_sbytes, dst + Cfg::kScaleBase + b * 256, v);
+      mx_dma4(isb ? b_scales : g.a_scales, isb ? b_sbytes : a_sbytes, dst + Cfg::kScaleBase + b * 256, v);
     }
   };
 
