@@ -66,11 +66,14 @@ __device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
 
 // Loads straight into LDS: lane i of the wave brings 16 (4) bytes at byte offset voff to
 // dst + 16 i (4 i); an offset behind the buffer brings zeros.
+// STREAM: a line that nobody else reads (non-temporal).
+constexpr int kStream = 2;
 typedef __attribute__((address_space(3))) void *mx_lds_ptr;
+template <bool STREAM = false>
 __device__ __forceinline__ void mx_dma16(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst,
-      16, voff, 0, 0, 0);
+      16, voff, 0, 0, STREAM ? kStream : 0);
 }
 __device__ __forceinline__ void mx_dma4(const void *base, uint32_t bytes, uint8_t *dst, uint32_t voff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(

@@ -1,4 +1,4 @@
-// A whole MXFP4 expert layer for a few tokens (T <= 64, a decode step) in two or three kernels.
+// A whole MXFP4 expert layer for a few tokens (T <= 64, a decode step) in two to four kernels.
 //
 // At this size the layer is bound by reading the chosen experts' weights once (0.53 bytes per
 // element; 2.5 MB per expert at hidden size 2048 and expert size 768) and, below that, by
@@ -6,25 +6,37 @@
 // look-up only and are all under way at once, and no intermediate but the quantised rows.
 //
 //   1. k_few_route    routes the tokens (topk_device.h), a few per workgroup, and quantises x.
-//                     Left out for the smallest batches (few_fused): there every workgroup of
-//                     the next kernel routes and quantises for itself, in LDS.
+//                     Left out for one or two tokens (few_fused): there every workgroup of the
+//                     next kernel routes and quantises for itself, in LDS (one token 19.3 -> 16.8
+//                     us; at seven the repeated work costs 8 us more than the launch).
 //   2. k_few_gate_up  one workgroup per (expert in use, 32 columns of I): gate and up products
 //                     for all the expert's tokens, SwiGLU and re-quantisation: 32 columns are
 //                     one MX block.  The K dimension is split over the eight waves.  Every wave
-//                     finds its expert's rows itself from the T * k ids (ballots, no sorting);
-//                     one more workgroup lists all experts' rows for the next kernel meanwhile.
-//   3. k_few_down     one workgroup per 16 columns of H: its waves walk over the experts, add
-//                     weight * product into a token table in LDS (one per wave), and the tables
-//                     are summed in wave order.  Where there are few columns, several workgroups
-//                     share a tile's experts.  No atomics on sums: the result is deterministic.
-// An assignment (token t, choice j) is numbered f = j * T + t.  With at most 16 of them and no
-// fewer experts the last kernel groups nothing: every assignment is an expert with one row.
+//                     finds its expert's rows itself from the T * k ids (ballots, no sorting).
+//      With more than kGroupedRows assignments (few_grouped) k_few_group and the grouped GEMM
+//                     (mx_gemm_kernel.h) take its place: the first lists the experts in use and
+//                     their rows.  Its 5 us pay once the GEMM's rows come cheaper (8 of 128
+//                     experts a token: 9 tokens 42.5 us here, 47.0 grouped; 14 tokens 52.4 and
+//                     50.6).
+//   3. k_few_down     one workgroup per 16 columns of H: its waves walk over the assignments
+//                     (few_grouped: the experts in use), add weight * product into a token table
+//                     in LDS (one per wave), and the tables are summed in wave order.  Where there
+//                     are few columns, several workgroups share a tile.  No atomics on sums: the
+//                     result is deterministic.
+// An assignment (token t, choice j) is numbered f = j * T + t.
 //
 // Products: v_mfma_scale_f32_16x16x128_f8f6f4 with weight rows as the first operand and up to
-// 16 of the expert's tokens as the second, straight from global memory: lane (row, g) holds
-// the 16-byte block g of the row's 128-element step, so one load of a wave covers 16 rows x 64
-// bytes.  Loads are buffer loads, whose offsets behind the row's end or without a row give
-// zeros without a branch.
+// 16 of the expert's tokens as the second: lane (row, g) holds the 16-byte block g of the row's
+// 128-element step.  Tokens' rows come straight from global memory in that layout, through buffer
+// loads, whose offsets behind the row's end or without a row give zeros without a branch.
+// Weights pass through LDS: loaded in that layout 16 adjacent lanes ask for 16 rows, and a load
+// costs the address unit 64 accesses instead of 16 (one token 16.4 -> 14.0 us, seven 41 -> 38, 64 of
+// them 82 -> 78).  They are streamed (non-temporal) past the caches, where the other operands
+// stay: eight layers in turn, as a decode step reads them, take 42.1 us each for seven tokens
+// against 44.6; 64 tokens again and again 70 against 78, seven 39.9 against 38.2.
+//
+// Measured at H 2048, I 768, 8 of 128 experts a token: one token 14.0 us, seven 39.9 (2.9 TB/s),
+// 64 tokens 70 us (4.5 TB/s, nearly every expert's weights).
 #include <algorithm>
 #include <type_traits>
 
@@ -393,7 +405,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
       const int r = i * 8 + (lane >> 3), b = (lane & 7) ^ ((r >> 1) & 7);
       const int row = c0 + (r & 31) + (r >> 5) * a.I;
       const bool in = (b < per * 4) & (s0 * 4 + b < w13.nb);
-      mx_dma16(w13.codes, w13.cbytes, mine + i * 1024, in ? (uint32_t)(row * w13.nb + s0 * 4 + b) * 16u : kOut);
+      mx_dma16<true>(w13.codes, w13.cbytes, mine + i * 1024, in ? (uint32_t)(row * w13.nb + s0 * 4 + b) * 16u : kOut);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -500,7 +512,7 @@ constexpr int kDnDma = kDnCodes / 1024 + 2;
 // entry a wave takes a `parts`-th of the steps (parts > 1 with at most four entries).
 // W2's 16 rows of a window go straight to the wave's own part of LDS, the next window's while
 // this one is computed, with no barrier.  Taken to registers in the products' layout they cost
-// the address unit one access a lane, since 16 adjacent lanes hold 16 rows: XX.
+// the address unit one access a lane, since 16 adjacent lanes hold 16 rows (64 tokens: 29 us, here 25).
 // With several splits each workgroup leaves its sums in the workspace, and the last one to
 // arrive adds them up, in split order whoever it is.
 // The SwiGLU rows are in assignment order, or (grouped) in expert order.
@@ -515,7 +527,7 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane & 15, g = lane >> 4;
   const int R = a.T * a.k;
-  const int most = min(a.E, R);  // entries
+  const int most = GROUPED ? min(a.E, R) : R;  // entries
   const int parts = most > 4 || splits > 1 ? 1 : most > 2 ? 2 : 4;
   const int tile = blockIdx.x / splits, split = blockIdx.x - tile * splits;
   const int part = wave % parts, stride = splits * kDnWaves / parts;
@@ -525,23 +537,26 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   const int c0 = tile * 16;
   const Mat h = matrix(ws.h_codes, ws.h_scales, 0, R, a.I);
   float *mine = table + wave * a.T * 16;
-  // the wave's entries, one per lane (at most 1024 / 16 of them): expert, first row, rows
+  // the wave's entries, 64 at a time, one per lane: expert, first row, rows
   int le = -1, lr = 0, ln = 0;
-  const int i0 = (split * kDnWaves + wave) / parts + lane * stride;
-  const int na = GROUPED ? *ws.n_active : R;  // (arrives with the entries, not before them)
-  if (i0 < (GROUPED ? most : R)) {
-    if (!GROUPED) {
-      le = ws.id[i0];
-      lr = i0;
-      ln = le < 0 ? 0 : 1;
-    } else {
-      le = ws.act_e[i0];
-      lr = ws.act_row[i0];
-      ln = ws.act_row[i0 + 1] - lr;
+  const int first = (split * kDnWaves + wave) / parts;
+  const auto load_entries = [&](int from) __attribute__((always_inline)) {
+    const int i = first + (from + lane) * stride;
+    if (i < most) {
+      if (!GROUPED) {
+        le = ws.id[i];
+        lr = i;
+        ln = le < 0 ? 0 : 1;
+      } else {  // (behind the experts in use: not written, not used)
+        le = ws.act_e[i];
+        lr = ws.act_row[i];
+        ln = ws.act_row[i + 1] - lr;
+      }
     }
-  }
-  const int count = __popcll(__ballot(i0 < na)) * windows;
-  if (i0 >= na) le = -1, ln = 0;
+  };
+  load_entries(0);
+  const int na = GROUPED ? __builtin_amdgcn_readfirstlane(*ws.n_active) : R;
+  const int count = (first < na ? (na - first + stride - 1) / stride : 0) * windows;
   for (int i = lane; i < a.T * 4; i += 64) reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
   // LDS position 16 p (p = 64 i + lane) holds block (p % 24) ^ (row / 2 % 8) of row p / 24: the 16
   // rows' same block then lies in 16 different groups of banks
@@ -559,8 +574,10 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   // item c: entry c / windows, window c % windows (counted up alongside, ic and iw)
   int ic = 0, iw = 0;
   const auto next_item = [&]() __attribute__((always_inline)) -> Item {
-    const Item it{__builtin_amdgcn_readlane(le, ic), __builtin_amdgcn_readlane(lr, ic),
-                  __builtin_amdgcn_readlane(ln, ic), (iw * parts + part) * per};
+    const int i = ic & 63;
+    if (i == 0 && ic > 0 && iw == 0) load_entries(ic);
+    const Item it{__builtin_amdgcn_readlane(le, i), __builtin_amdgcn_readlane(lr, i),
+                  __builtin_amdgcn_readlane(ln, i), (iw * parts + part) * per};
     if (++iw == windows) iw = 0, ++ic;
     return it;
   };
@@ -572,7 +589,7 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
     for (int i = 0; i < kDnCodes / 1024; ++i) {
       const int b = it.s0 * 4 + at_b[i];
       const bool in = live & (at_row[i] >= 0) & (at_b[i] < per * 4) & (b < w2.nb);
-      mx_dma16(w2.codes, w2.cbytes, dst + i * 1024, in ? (uint32_t)(at_row[i] * w2.nb + b) * 16u : kOut);
+      mx_dma16<true>(w2.codes, w2.cbytes, dst + i * 1024, in ? (uint32_t)(at_row[i] * w2.nb + b) * 16u : kOut);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

@@ -113,7 +113,6 @@ __device__ __forceinline__ void mx_store8(void *base, uint32_t bytes, uint32_t v
 // would stay in L2 push out the codes that neighbouring tiles share.  dW of 64 experts (768 x 2048,
 // FP32, 32768 rows): 139 -> 105 us; dX in FP32 85 -> 66; BF16 rows 67 -> 63 with 128 x 128
 // tiles, unchanged with 256 x 256.  Codes and scale bytes are part lines and stay cached.
-constexpr int kStream = 2;
 __device__ __forceinline__ void mx_store4(void *base, uint32_t bytes, uint32_t voff, uint32_t v) {
   __builtin_amdgcn_raw_buffer_store_b32(
       v, __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000), voff,

@@ -499,6 +499,69 @@ def test_few_strides_nan_and_rows_left(gpu_lib):
     assert empty.shape == (0, H)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (64, 3, 2, 96, 1632), (40, 6, 2, 64, 1632), (36, 2, 2, 4128, 32), (24, 3, 3, 2112, 64), (1, 6, 3, 64, 3136),
+    (25, 9, 3, 32, 800), (64, 90, 1, 64, 64)])
+def test_few_many_rows_and_windows(gpu_lib, T, E, k, H, I):
+    """More than 16 rows of an expert, and more of either matrix's K than a wave holds at once."""
+    test_few(gpu_lib, T, E, k, H, I)
+
+
+def random_mx(gpu_lib, rows, K):
+    """Random codes under scales 2^-7 .. 1, made on the GPU."""
+    codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((rows, gpu_lib.mxfp4_scale_stride(K)), dtype=torch.uint8, device="cuda")
+    scales[:, :K // 32] = torch.randint(120, 128, (rows, K // 32), dtype=torch.uint8, device="cuda")
+    return gpu_lib.MXFP4(codes, scales, rows, K)
+
+
+def test_few_more_experts_than_a_pass_holds(gpu_lib):
+    """1024 experts in use and one workgroup a column tile.  The whole is the sum of its quarters:
+    FP32 sums of 32 terms in another order, each off by at most 32 2^-24 of the terms' sum."""
+    T, E, k, H, I = 64, 1024, 32, 2080, 32
+    w = gpu_lib.MXExpertWeights(random_mx(gpu_lib, E * 2 * I, H), random_mx(gpu_lib, E * H, I), E, H, I)
+    x = torch.randn(T, H, device="cuda")
+    ids = torch.stack([torch.randperm(E, device="cuda")[:k] for _ in range(T // 2)]).int()
+    ids = torch.cat([torch.arange(T // 2 * k, device="cuda").reshape(T // 2, k).int() % E, ids])  # every expert
+    wts = torch.rand(T, k, device="cuda") + 0.1
+    o = dict(out_dtype=torch.float32)
+    out = gpu_lib.mx_moe_few(x, None, w, k, topk_ids=ids, topk_w=wts, **o)
+    part = [gpu_lib.mx_moe_few(x, None, w, 8, topk_ids=ids[:, i:i + 8].contiguous(),
+                               topk_w=wts[:, i:i + 8].contiguous(), **o).double() for i in range(0, k, 8)]
+    size = sum(p.abs() for p in part)
+    assert torch.unique(ids).numel() == E and size.min() > 0
+    assert ((out.double() - sum(part)).norm() / sum(part).norm()).item() <= 32 * 2.0 ** -24 * 4
+
+
+def test_weights_above_4_gib(gpu_lib):
+    """Experts on either side of 4 GiB of codes against the same two experts alone.  FP32 sums of
+    K / 64 partial sums, possibly by other tiles: off by at most K / 64 2^-24 of the terms' sum,
+    of which a random row's norm is at least a hundredth."""
+    E, H, I = 132, 8192, 4096
+    w13, w2 = random_mx(gpu_lib, E * 2 * I, H), random_mx(gpu_lib, E * H, I)
+    assert w13.codes.numel() > 1 << 32
+    pick = lambda m, n: gpu_lib.MXFP4(*(torch.cat([t[:n], t[-n:]]) for t in (m.codes, m.scales)), 2 * n, m.K)
+    two13, two2 = pick(w13, 2 * I), pick(w2, H)
+    R = 80
+    x = gpu_lib.mxfp4_quantize(torch.randn(R, H, device="cuda", dtype=torch.bfloat16))
+    far = torch.tensor([0] + [35] * (E - 1) + [R], dtype=torch.int32, device="cuda")
+    near = torch.tensor([0, 35, R], dtype=torch.int32, device="cuda")
+    f32 = dict(out_dtype=torch.float32)
+    got = gpu_lib.mxfp4_grouped_gemm(x, w13, far, E, 2 * I, M_cap=R, **f32)
+    ref = gpu_lib.mxfp4_grouped_gemm(x, two13, near, 2, 2 * I, M_cap=R, **f32)
+    tol = H / 64 * 2.0 ** -24 * 100
+    assert ((got - ref).norm(dim=1) <= tol * ref.norm(dim=1)).all() and ref.abs().max() > 0
+    xf = torch.randn(R // 2, H, device="cuda", dtype=torch.bfloat16)
+    wts = torch.rand(R // 2, 2, device="cuda")
+    for T in (1, 20, 40):  # each of the three ways through the layer
+        ids = torch.tensor([[E - 1, 0]], dtype=torch.int32, device="cuda").repeat(T, 1)
+        few = lambda m13, m2, n, ids: gpu_lib.mx_moe_few(xf[:T], None, gpu_lib.MXExpertWeights(m13, m2, n, H, I), 2,
+                                                         topk_ids=ids, topk_w=wts[:T].contiguous(), **f32)
+        got, ref = few(w13, w2, E, ids), few(two13, two2, 2, (ids > 0).int())
+        # (a sum next to a rounding border may take the other code: 0.3 of them in a row of 2 I)
+        assert ((got - ref).norm(dim=1) <= 5e-3 * ref.norm(dim=1)).all() and ref.abs().max() > 0
+
+
 # ----------------------------------------------------------------------------- streams and graphs
 
 def test_side_stream_and_two_calls_at_once(gpu_lib):
