@@ -109,6 +109,7 @@ nv4_status mx_padded_offsets(const int32_t *offsets, int nseg, int32_t *padded, 
  *   over [offsets[e], offsets[e+1]) (multiples of NV4_MX_SEGMENT, from
  *   mx_padded_offsets); C [E][N][ldc] gets A_e . B_e^T, zeros for an empty range.
  *   offsets   device int32 [E+1], 1 <= E <= 1024
+ * A, and an expert's part of B (GROUP_K: B), each stay below 4 GiB of codes.
  * No workspace.  Errors: EINVAL, EALIGN (K % 32, misaligned operands), EUNSUPPORTED
  * (a row index, q_out or SwiGLU with GROUP_K; q_out without SwiGLU), EHIP.
  */
@@ -118,7 +119,7 @@ nv4_status mxfp4_grouped_gemm(const nv4_mx_tensor *A, const nv4_mx_tensor *B, co
 
 /*
  * mx_moe_few -- a whole MXFP4 expert layer for at most NV4_MX_FEW_TOKENS tokens (a decode
- * step), in three kernels: routing and activation quantisation; gate and up products,
+ * step), in two to four kernels: routing and activation quantisation; gate and up products,
  * SwiGLU, re-quantisation; down product and weighted sum.
  *   out[t] = sum_j w[t][j] * W2_e . Q(silu(W13g_e . Q(x[t])) * (W13u_e . Q(x[t]))), e = id[t][j]
  * with every sum in FP32 and Q the quantisation above: the layer that moe_permute,
@@ -133,6 +134,8 @@ nv4_status mxfp4_grouped_gemm(const nv4_mx_tensor *A, const nv4_mx_tensor *B, co
  *   w13 [E*2I][H], w2 [E*H][I]   H % 32 == 0, I % 32 == 0
  *   flags            NV4_RENORM or 0
  *   out              [T][H], BF16 or FP32
+ *   dev_status       NV4_DS_NAN_LOGIT, NV4_DS_BAD_EXPERT, and NV4_DS_NONFINITE for x (a SwiGLU
+ *                    value past FP32's range makes the token's results NaN without it)
  *   ws, ws_bytes     mx_moe_few_workspace() bytes, 256-byte aligned; calls that share one
  *                    must not overlap
  * Errors: EINVAL, EALIGN, EUNSUPPORTED (T > NV4_MX_FEW_TOKENS, E > 1024, k > min(E, 32)),

@@ -418,7 +418,6 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
   load_w(wave * per);
   const int slot = tid >> 4, cc = (tid & 15) * 2;
   const int hsld = sc_stride(a.I);
-  bool bad = false;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   for (int q = 0; q < n; q += 16) {
@@ -490,14 +489,12 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
       uint32_t c = mx_pack_f32<0>(0u, h[0], h[1], mx_scale_value(byte));
       if (byte == kMxNan) c = 0u;
       if (q + slot < n) {
-        bad |= byte == kMxNan;
         const int64_t r = rows[wave][q + slot];
         ws.h_codes[r * (a.I / 2) + (c0 + cc) / 2] = (uint8_t)c;
         if ((tid & 15) == 0) ws.h_scales[r * hsld + c0 / 32] = (uint8_t)byte;
       }
     }
   }
-  if (bad && a.dev_status) atomicOr(a.dev_status, kDsNonFinite);
 }
 
 // ---------------------------------------------------------------- 3. down

@@ -112,6 +112,8 @@ __global__ __launch_bounds__(256) void k_mx_cols(MxQuantArgs a, int chunks, int6
     // the last segment whose padded start is <= p0, every thread a candidate: one round trip for
     // up to 256 segments where a binary search takes eight (with the loads below: 131072 x 2048
     // BF16 159 -> 139 us, gathered from 16384 rows 130 -> 91)
+    if (tid < 4) s_seg[tid] = 0;  // (starts that do not begin at 0 leave an empty segment)
+    __syncthreads();
     for (int lo = 0, n = a.nseg;;) {
       const int step = (n + 255) / 256, at = lo + tid * step;
       if (tid * step < n) {

@@ -414,7 +414,7 @@ def mx_moe_few(x: torch.Tensor, logits: torch.Tensor | None, w: MXExpertWeights,
                out_dtype=torch.bfloat16, out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
                rule: int = NV4_MX_FLOOR, dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The layer of ``mx_moe_forward`` for at most NV4_MX_FEW_TOKENS tokens (a decode step) in
-    three kernels: x [T, H], logits FP32 [T, E] -> out [T, H].  With logits None, topk_ids
+    two to four kernels: x [T, H], logits FP32 [T, E] -> out [T, H].  With logits None, topk_ids
     (int32 [T, k]) and topk_w (FP32) are the routing; otherwise they receive it when given."""
     ldx = _matrix(x, "x")
     T, H = x.shape

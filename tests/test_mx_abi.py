@@ -129,6 +129,15 @@ def test_gemm_refuses(lib, want, o):
     assert lib.nv4_last_error().startswith(b"mxfp4_grouped_gemm")
 
 
+def test_sizes_behind_32_bit_offsets_are_refused(lib):
+    n = 1 << 22
+    assert _gemm(lib, E=1, N=n, ldc=n, M=1, A=mx(100, 2112), B=mx(n, 2112)) == EINVAL  # one expert above 4 GiB
+    assert b"4 GiB" in lib.nv4_last_error()
+    seg = dict(layout=2, so=P, sp=P, out=mx(96, 256))
+    assert _quantize(lib, ldx=n + 8, **seg) == EINVAL and b"2^22" in lib.nv4_last_error()
+    assert _quantize(lib, ldx=n + 8, layout=3, nseg=2, out=mx(192, 32)) == EINVAL
+
+
 def _few(lib, **o):
     d = dict(x=P, xt=0, ldx=64, lg=P, T=3, E=4, k=2, fl=0, ids=None, w=None, w13=mx(4 * 64, 64), w2=mx(4 * 64, 32), H=64,
              I=32, rule=0, out=P, ot=0, ldo=64, ws=P, wsb=1 << 20)
