@@ -15,22 +15,29 @@ hipError_t launch_mx_gemm_small(const MxGemmArgs &g, hipStream_t stream);
 namespace {
 
 // 256-, 128- or 64-row tiles (wider ones do more products per byte, narrower ones waste fewer
-// rows behind an expert's last and give more workgroups).  The row counts stay on the device:
-// the choice goes by their mean.  Measured in us, 64 x 128 / 128 x 128 / 256 x 256 tiles:
-//   gate and up, K = 2048, N = 768, 128 experts of  32 rows  38.6 / 43.5 / 64.2
-//                                                   48       43.3 / 44.2 / 65.6
-//                                                   64       53.4 / 44.9 / 65.2
-//                                                  128       81.8 / 69.8 / 70.7
-//                                                  160       91.4 / 83.0 / 73.5
-//                                                  384        202 /  154 /  136
-//   one expert, K = N = 2048, rows 2048             14.2 / 17.4 / 21.9   (512, 256, 64 tiles)
-//                                  4096             23.3 / 20.3 / 24.4
-//                                  8192             40.9 / 33.0 / 28.1
+// rows behind an expert's last; the narrowest streams its weights).  The row counts stay on the
+// device: the choice goes by their mean.  Measured in us with several layers' weights in turn,
+// 64 x 128 / 128 x 128 / 256 x 256 tiles:
+//   gate and up, K = 2048, N = 768, 128 experts of  16 rows  47.9 / 56.9 / 79.4
+//                                                   32       53.8 / 58.0 / 79.4
+//                                                   64       67.8 / 69.8 / 78.2
+//                                                   96       98.7 / 79.6 / 99.3
+//                                                  144      118.2 / 96.3 / 100
+//                                                  192      155.2 /  116 / 104
+//                                                  384      268.8 /  172 / 166
+//   K = 768, N = 2048, 64 experts of                32       23.0 / 23.2 / 28.7
+//                                                   64       27.6 / 26.6 / 30.1
+//                                                  128       41.2 / 35.8 / 41.9
+//                                                  160       48.9 / 42.4 / 42.6
+//                                                  256       68.9 / 51.4 / 44.7
+//   one expert, K = N = 2048, rows                 1024      17.6 / 15.9 / 22.9   (32 large tiles)
+//                                                  4096      35.9 / 19.7 / 24.4   (128)
+//                                                  8192      63.5 / 33.0 / 30.9   (256)
 hipError_t launch_rows(const MxGemmArgs &g, hipStream_t stream) {
-  const int64_t n = g.epilogue == NV4_EPI_SWIGLU ? 2 * g.N : g.N, cus = device_cu_count();
-  const auto tiles = [&](int64_t bm, int64_t bn) { return (g.M_cap / bm + g.E / 2) * ((n + bn - 1) / bn); };
-  if (g.M_cap >= 144 * (int64_t)g.E && tiles(256, 256) >= cus) return launch_mx_gemm_large(g, stream);
-  if (g.M_cap >= 50 * (int64_t)g.E && tiles(128, 128) > cus) return launch_mx_gemm_medium(g, stream);
+  const int64_t n = g.epilogue == NV4_EPI_SWIGLU ? 2 * g.N : g.N;
+  const int64_t large = (g.M_cap / 256 + g.E / 2) * ((n + 255) / 256);
+  if (g.M_cap >= 160 * (int64_t)g.E && large >= device_cu_count()) return launch_mx_gemm_large(g, stream);
+  if (g.M_cap >= 64 * (int64_t)g.E) return launch_mx_gemm_medium(g, stream);
   return launch_mx_gemm_small(g, stream);
 }
 
@@ -39,7 +46,8 @@ hipError_t launch_rows(const MxGemmArgs &g, hipStream_t stream) {
 hipError_t launch_mx_gemm(const MxGemmArgs &g, hipStream_t stream) {
   if (g.group_mode != NV4_GROUP_K) return launch_rows(g, stream);
   // weight gradients: no row is wasted, so the large tile as soon as it fills the chip (64
-  // experts of 768 x 2048: 138 us against 160)
+  // experts of 768 x 2048, FP32 results of 32768 rows: 105 us against 106; 128 of 1536 x 2048 and
+  // 131072 rows: 572 against 630)
   const int64_t large = (int64_t)g.E * ((g.a_rows + 255) / 256) * ((g.b_rows + 255) / 256);
   return large >= device_cu_count() ? launch_mx_gemm_large(g, stream) : launch_mx_gemm_medium(g, stream);
 }
