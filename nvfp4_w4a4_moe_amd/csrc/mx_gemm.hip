@@ -18,25 +18,26 @@ namespace {
 // rows behind an expert's last; the narrowest streams its weights).  The row counts stay on the
 // device: the choice goes by their mean.  Measured in us with several layers' weights in turn,
 // 64 x 128 / 128 x 128 / 256 x 256 tiles:
-//   gate and up, K = 2048, N = 768, 128 experts of  16 rows  47.9 / 56.9 / 79.4
-//                                                   32       53.8 / 58.0 / 79.4
-//                                                   64       67.8 / 69.8 / 78.2
-//                                                   96       98.7 / 79.6 / 99.3
-//                                                  144      118.2 / 96.3 / 100
-//                                                  192      155.2 /  116 / 104
-//                                                  384      268.8 /  172 / 166
-//   K = 768, N = 2048, 64 experts of                32       23.0 / 23.2 / 28.7
-//                                                   64       27.6 / 26.6 / 30.1
-//                                                  128       41.2 / 35.8 / 41.9
-//                                                  160       48.9 / 42.4 / 42.6
-//                                                  256       68.9 / 51.4 / 44.7
-//   one expert, K = N = 2048, rows                 1024      17.6 / 15.9 / 22.9   (32 large tiles)
-//                                                  4096      35.9 / 19.7 / 24.4   (128)
-//                                                  8192      63.5 / 33.0 / 30.9   (256)
+//   gate and up, K = 2048, N = 768, 128 experts of  16 rows  47.4 / 55.6 / 69.6
+//                                                   32       53.3 / 56.5 / 68.1
+//                                                   64       67.3 / 67.8 / 71.2
+//                                                   96       98.2 / 79.4 / 86.2
+//                                                  128        111 / 83.1 / 88.2
+//                                                  144        116 / 95.0 / 93.2
+//                                                  192        154 /  114 /  105
+//                                                  384        266 /  172 /  152
+//   K = 768, N = 2048, 64 experts of                32       21.4 / 22.3 / 26.1
+//                                                   64       26.4 / 27.3 / 27.6
+//                                                  128       39.2 / 35.6 / 37.8
+//                                                  160       45.4 / 41.8 / 42.5
+//                                                  256       64.0 / 51.3 / 44.1
+//   one expert, K = N = 2048, rows                 1024      17.6 / 15.7 / 22.9   (32 large tiles)
+//                                                  4096      35.2 / 19.6 / 24.6   (128)
+//                                                  8192      62.7 / 32.9 / 31.0   (256)
 hipError_t launch_rows(const MxGemmArgs &g, hipStream_t stream) {
   const int64_t n = g.epilogue == NV4_EPI_SWIGLU ? 2 * g.N : g.N;
   const int64_t large = (g.M_cap / 256 + g.E / 2) * ((n + 255) / 256);
-  if (g.M_cap >= 160 * (int64_t)g.E && large >= device_cu_count()) return launch_mx_gemm_large(g, stream);
+  if (g.M_cap >= 144 * (int64_t)g.E && large >= device_cu_count()) return launch_mx_gemm_large(g, stream);
   if (g.M_cap >= 64 * (int64_t)g.E) return launch_mx_gemm_medium(g, stream);
   return launch_mx_gemm_small(g, stream);
 }

@@ -566,6 +566,13 @@ void k_mx_gemm(MxGemmArgs g) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
+  // A wave without rows of the tile only loads and keeps the barriers
+  const auto idle = [&](auto P, int st, int p_st, bool live, bool of_next) MX_INLINE {
+    constexpr int N = decltype(P)::value;
+    if (st + 1 >= S) mx_wait_vm<(S - 2) * Cfg::kDma>();
+    mx_barrier();
+    load_stage(N == 0 ? ring0 : N == 1 ? ring1 : N == 2 ? ring2 : ring3, p_st, live, of_next);
+  };
   // stage st of the tile; refills its slot with stage p_st of the loading tile
   const auto stage = [&](auto P, int st, int p_st, bool live, bool of_next) MX_INLINE {
     constexpr int N = decltype(P)::value;
@@ -633,31 +640,45 @@ void k_mx_gemm(MxGemmArgs g) {
       mx_barrier();
       p_next(it + 1);
       if (gather && p_live) load_index(pj);
-      read_first(ring0);
-      // stages that refill their slot from this tile, then those that fill it from the next
-      const int own = std::max(cj.nst - S, 0);
+      // An expert's last tile costs its rows rounded up to a wave's, not to a tile: the waves behind
+      // them leave the matrix cores to the others (128 experts of 1024 rows, gate and up: 305 us if
+      // they multiply too, 295 so).
+      const auto run = [&](auto ACTIVE) MX_INLINE {
+        // stages that refill their slot from this tile, then those that fill it from the next
+        const int own = std::max(cj.nst - S, 0);
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const int lo = part ? own : 0, hi = part ? cj.nst : own;
-        if (part && p_live) {
-          if (gather) {  // behind the indices: the loads of `own` stages
-            if (own >= S - 1) mx_wait_vm<(S - 1) * Cfg::kDma>();
-            else mx_wait_vm<0>();
+        for (int part = 0; part < 2; ++part) {
+          const int lo = part ? own : 0, hi = part ? cj.nst : own;
+          if (part && p_live) {
+            if (gather) {  // behind the indices: the loads of `own` stages
+              if (own >= S - 1) mx_wait_vm<(S - 1) * Cfg::kDma>();
+              else mx_wait_vm<0>();
+            }
+            p_setup();
           }
-          p_setup();
-        }
 #pragma unroll 1
-        for (int st = lo / S * S; st < hi; st += S) {
-          const auto one = [&](auto P) MX_INLINE {
-            constexpr int N = decltype(P)::value;
-            const int s = st + N;
-            if (N < S && s >= lo && s < hi) stage(P, s, part ? N : s + S, part == 0 || (p_live && N < pj.nst), part);
-          };
-          one(std::integral_constant<int, 0>{});
-          one(std::integral_constant<int, 1>{});
-          if constexpr (S > 2) one(std::integral_constant<int, 2>{});
-          if constexpr (S > 3) one(std::integral_constant<int, 3>{});
+          for (int st = lo / S * S; st < hi; st += S) {
+            const auto one = [&](auto P) MX_INLINE {
+              constexpr int N = decltype(P)::value;
+              const int s = st + N;
+              if (N < S && s >= lo && s < hi) {
+                const bool live = part == 0 || (p_live && N < pj.nst);
+                if constexpr (decltype(ACTIVE)::value) stage(P, s, part ? N : s + S, live, part);
+                else idle(P, s, part ? N : s + S, live, part);
+              }
+            };
+            one(std::integral_constant<int, 0>{});
+            one(std::integral_constant<int, 1>{});
+            if constexpr (S > 2) one(std::integral_constant<int, 2>{});
+            if constexpr (S > 3) one(std::integral_constant<int, 3>{});
+          }
         }
+      };
+      if (GROUP == NV4_GROUP_K || cj.m0 + wm * FM * 32 < cj.m_end) {
+        read_first(ring0);
+        run(std::true_type{});
+      } else {
+        run(std::false_type{});
       }
       // a short tile did not use every slot
       if (cj.nst < S) {
