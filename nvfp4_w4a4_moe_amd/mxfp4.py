@@ -54,6 +54,9 @@ _SIGS.update({
 })
 
 
+_U8 = torch.uint8
+
+
 def mxfp4_scale_stride(K: int) -> int:
     """Bytes between two rows of scales: K/32 rounded up to a multiple of 4."""
     return (K // 32 + 3) // 4 * 4
@@ -75,10 +78,11 @@ class MXFP4:
                      torch.empty((rows, mxfp4_scale_stride(K)), dtype=torch.uint8, device=device), rows, K)
 
     def c(self) -> MXTensor:
-        for t, cols in ((self.codes, self.K // 2), (self.scales, mxfp4_scale_stride(self.K))):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != self.rows * cols:
-                raise ValueError(f"MXFP4 [{self.rows}, {self.K}] needs contiguous uint8 codes and scales of its shape")
-        return MXTensor(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K)
+        c, s, rows, K = self.codes, self.scales, self.rows, self.K
+        if not (c.dtype is s.dtype is _U8 and c.is_contiguous() and s.is_contiguous() and
+                c.numel() == rows * (K // 2) and s.numel() == rows * ((K // 32 + 3) // 4 * 4)):
+            raise ValueError(f"MXFP4 [{rows}, {K}] needs contiguous uint8 codes and scales of its shape")
+        return MXTensor(c.data_ptr(), s.data_ptr(), rows, K)
 
 
 # ----------------------------------------------------------------------------- arguments
@@ -95,9 +99,10 @@ def _float(t: torch.Tensor, name: str) -> int:
 
 def _matrix(t: torch.Tensor, name: str) -> int:
     """The row stride of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return max(t.stride(0), t.shape[1])
+    return max(stride[0], shape[1])
 
 
 def _ints(t: torch.Tensor | None, name: str, n: int | None = None):
@@ -125,22 +130,21 @@ class _Call:
             if t is not None and t.get_device() != index:
                 raise ValueError(f"tensors on {first.device} and {t.device} in one call")
         self.device = first.device
-        if index < 0 or self.device.type != "cuda":
+        if not first.is_cuda:
             raise ValueError(f"tensors must be on a GPU, not on {first.device}")
         if stream is not None and stream.device != self.device:
             raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
         self.index, self.given = index, stream
         self.stream = _raw_stream(index) if stream is None else stream.cuda_stream
 
-    def empty(self, shape, dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+    def empty(self, dtype, *shape) -> torch.Tensor:
+        t = torch.empty(*shape, dtype=dtype, device=self.device)
         if self.given is not None:
             t.record_stream(self.given)
         return t
 
     def mx(self, rows: int, K: int) -> MXFP4:
-        return MXFP4(self.empty((rows, K // 2), torch.uint8), self.empty((rows, mxfp4_scale_stride(K)), torch.uint8),
-                     rows, K)
+        return MXFP4(self.empty(_U8, rows, K // 2), self.empty(_U8, rows, (K // 32 + 3) // 4 * 4), rows, K)
 
     def __call__(self, fn, *args):
         if torch.cuda.current_device() == self.index:
@@ -173,7 +177,7 @@ def mx_padded_offsets(offsets: torch.Tensor, out: torch.Tensor | None = None, st
     """Segment starts with every segment padded to NV4_MX_SEGMENT, from int32 offsets [nseg+1]."""
     call = _Call(stream, offsets, out)
     if out is None:
-        out = call.empty(offsets.shape, torch.int32)
+        out = call.empty(torch.int32, *offsets.shape)
     n = offsets.numel()
     call(load().mx_padded_offsets, _ints(offsets, "offsets"), n - 1, _ints(out, "out", n))
     return out
@@ -214,10 +218,12 @@ def mxfp4_dequantize(q: MXFP4, out_dtype=torch.bfloat16, out: torch.Tensor | Non
     """The values of q, [rows, K] BF16 or FP32 (both hold them exactly)."""
     call = _Call(stream, q.codes, q.scales, out)
     if out is None:
-        out = call.empty((q.rows, q.K), out_dtype)
-    ldo = _matrix(out, "out")
-    if out.shape != (q.rows, q.K):
-        raise ValueError(f"out must be [{q.rows}, {q.K}]")
+        out = call.empty(out_dtype, q.rows, q.K)
+        ldo = q.K
+    else:
+        ldo = _matrix(out, "out")
+        if out.shape != (q.rows, q.K):
+            raise ValueError(f"out must be [{q.rows}, {q.K}]")
     call(load().mxfp4_dequantize, q.c(), out.data_ptr(), _float(out, "out"), ldo)
     return out
 
@@ -240,8 +246,6 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
         shape = (M_cap, N)
         if a_rows is not None and a_rows.numel() < M_cap:
             raise ValueError("a_rows must name a row of A for each of the M_cap rows")
-    if C is None and want_c:
-        C = call.empty(shape, out_dtype)
     ldc, ctype = 0, NV4_F32
     if C is not None:
         ctype = _float(C, "C")
@@ -249,6 +253,9 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
                 C.shape[-1] != shape[-1] or group_mode == NV4_GROUP_K and (C.shape[0] != E or not C.is_contiguous()):
             raise ValueError(f"C must be {list(shape)} with contiguous rows")
         ldc = max(C.stride(-2), C.shape[-1])
+    elif want_c:
+        C = call.empty(out_dtype, *shape)
+        ctype, ldc = _float(C, "C"), shape[-1]
     call(load().mxfp4_grouped_gemm, A.c(), B.c(), _ints(offsets, "offsets", E + 1), E, M_cap, N,
          _ints(a_rows, "a_rows"), group_mode, epilogue, _p(C), ctype, ldc, None if q_out is None else q_out.c(), rule)
     return C
@@ -428,11 +435,11 @@ def mx_moe_few(x: torch.Tensor, logits: torch.Tensor | None, w: MXExpertWeights,
     if topk_w is not None and (topk_w.dtype != torch.float32 or not topk_w.is_contiguous() or topk_w.numel() != T * k):
         raise ValueError(f"topk_w must be contiguous FP32 [{T}, {k}]")
     if out is None:
-        out = call.empty((T, H), out_dtype)
+        out = call.empty(out_dtype, T, H)
     elif out.shape != x.shape:
         raise ValueError(f"out must be [{T}, {H}]")
     if ws is None:
-        ws = call.empty(max(_few_workspace(T, w.E, k, H, w.I), 256), torch.uint8)
+        ws = call.empty(_U8, max(_few_workspace(T, w.E, k, H, w.I), 256))
     elif ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be contiguous uint8")
     call(load().mx_moe_few, x.data_ptr(), _float(x, "x"), ldx, _p(logits), T, w.E, k, flags,
