@@ -67,7 +67,8 @@ int64_t mxfp4_scale_stride(int64_t K);
  *                      NV4_MX_SEGMENT columns (seg_padded_offsets of mx_padded_offsets);
  *                      out->K >= rows + 127 * nseg, a multiple of 128; columns at and
  *                      after seg_padded_offsets[nseg] are not written.
- *                    NV4_ROWS_AND_COLS: NV4_COLS into out and NV4_ROWS into out_rows.
+ *                    NV4_ROWS_AND_COLS: NV4_COLS into out and NV4_ROWS into out_rows, of
+ *                      which rows behind the last segment are not written.
  *                    NV4_COLS_BATCHED: nseg equal matrices of m = rows/nseg rows
  *                      (m % 32 == 0); out [nseg*K][m] holds each transposed.
  *   nseg, seg_offsets, seg_padded_offsets   device int32 [nseg+1], for NV4_COLS and

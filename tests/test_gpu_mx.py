@@ -130,6 +130,68 @@ def test_quantize_cols(gpu_lib, counts, K, f32):
                 check_codes(q.rows_out, x)
 
 
+@pytest.mark.parametrize("nseg", [257, 1000, 70000])
+def test_quantize_cols_many_segments(gpu_lib, nseg):
+    """Most of them empty, more than one and two passes of a workgroup's search; and rows behind
+    the last segment, which neither direction writes."""
+    r = synth.rng(nseg)
+    counts = np.zeros(nseg, np.int64)
+    counts[r.choice(nseg, 40, replace=False)] = r.integers(1, 300, 40)
+    counts[[0, nseg - 1]] = [0, 5]
+    off, K = np.concatenate([[0], np.cumsum(counts)]), 96
+    R, extra = int(off[-1]), 70
+    x = wide((R + extra, K), 7)
+    po = M.padded_offsets(off)
+    P = int(po[-1])
+    if nseg <= 1024:
+        assert np.array_equal(host(gpu_lib.mx_padded_offsets(dev_i32(off))), po)
+    c, b = M.quantize(M.by_segment(x, off))
+    for layout in (gpu_lib.NV4_COLS, gpu_lib.NV4_ROWS_AND_COLS):
+        rows_out = None
+        if layout == gpu_lib.NV4_ROWS_AND_COLS:
+            rows_out = gpu_lib.MXFP4.empty(R + extra, K)
+            rows_out.codes.fill_(0xAA)
+            rows_out.scales.fill_(0xAA)
+        q = gpu_lib.mxfp4_quantize(dev_bf16(x), layout=layout, nseg=nseg, seg_offsets=dev_i32(off),
+                                   seg_padded_offsets=dev_i32(po), out_rows=rows_out)
+        gc, gb = Q.unpack_codes(host(q.codes[:, :P // 2])), host(q.scales[:, :P // 32])
+        assert np.array_equal(gc, c) and np.array_equal(gb, b)
+        if rows_out is not None:
+            check_codes(gpu_lib.MXFP4(rows_out.codes[:R], rows_out.scales[:R], R, K), x[:R])
+            assert (rows_out.codes[R:] == 0xAA).all() and (rows_out.scales[R:] == 0xAA).all()
+
+
+def test_offsets_behind_32_bits(gpu_lib):
+    """More than 2^32 bytes of every large operand but the codes: the last rows against a call with
+    those rows alone."""
+    K, rows, tail = 2048, (1 << 20) + 4096 + 77, 300
+    x = torch.randn(rows, K, device="cuda", dtype=torch.bfloat16)
+    q, t = gpu_lib.mxfp4_quantize(x), gpu_lib.mxfp4_quantize(x[-tail:])
+    assert x.numel() * 2 > 1 << 32 and same_bits(q.codes[-tail:], t.codes) and same_bits(q.scales[-tail:], t.scales)
+    f32 = gpu_lib.mxfp4_dequantize(q, torch.float32)
+    assert torch.equal(f32[-tail:], gpu_lib.mxfp4_dequantize(t, torch.float32))
+    off = dev_i32(np.array([0, rows - tail, rows]))
+    po = gpu_lib.mx_padded_offsets(off)
+    seg = dict(layout=gpu_lib.NV4_ROWS_AND_COLS, nseg=2, seg_offsets=off, seg_padded_offsets=po)
+    one = dev_i32(np.array([0, tail]))
+    ref = gpu_lib.mxfp4_quantize(x[-tail:], layout=gpu_lib.NV4_COLS, nseg=1, seg_offsets=one,
+                                 seg_padded_offsets=gpu_lib.mx_padded_offsets(one))
+    for wide_x in (x, f32):
+        c = gpu_lib.mxfp4_quantize(wide_x, **seg)
+        start, end = po[1].item(), po[2].item()
+        if wide_x is x:
+            assert torch.equal(c.codes[:, start // 2:end // 2], ref.codes[:, :(end - start) // 2])
+            assert torch.equal(c.scales[:, start // 32:end // 32], ref.scales[:, :(end - start) // 32])
+        assert same_bits(c.rows_out.codes[-tail:], t.codes)
+    del f32, c
+    w = gpu_lib.mxfp4_quantize(torch.randn(2 * 2048, K, device="cuda", dtype=torch.bfloat16))
+    y = gpu_lib.mxfp4_grouped_gemm(q, w, off, 2, 2048)
+    ref = gpu_lib.mxfp4_grouped_gemm(t, gpu_lib.MXFP4(w.codes[2048:], w.scales[2048:], 2048, K), one, 1, 2048)
+    # (other tiles may sum K in another order: at most K / 64 partial sums)
+    assert y.numel() * 4 > 1 << 32
+    assert ((y[-tail:] - ref).norm(dim=1) <= K / 64 * 2.0 ** -23 * 100 * ref.norm(dim=1)).all()
+
+
 @pytest.mark.parametrize("nseg,m,K", [(1, 32, 32), (3, 96, 64), (2, 128, 160), (5, 288, 96)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_quantize_cols_batched(gpu_lib, nseg, m, K, f32):
@@ -581,6 +643,50 @@ def test_side_stream_and_two_calls_at_once(gpu_lib):
     torch.cuda.synchronize()
     for got, want in outs:
         assert same_bits(got, want)
+
+
+def test_graphs_that_share_a_workspace(gpu_lib):
+    """Two captured batches of different sizes and an eager one in one workspace, in turn."""
+    E, k, H, I = 24, 4, 544, 96
+    x, lg, w, *_ = few_case(gpu_lib, 64, E, k, H, I)
+    xd, ld = dev_bf16(x), dev_f32(lg)
+    ws = torch.empty(gpu_lib.load().mx_moe_few_workspace(64, E, k, H, I), dtype=torch.uint8, device="cuda")
+    want = {T: gpu_lib.mx_moe_few(xd[:T], ld[:T], w, k) for T in (1, 2, 9, 30, 64)}
+    out = {T: torch.empty((T, H), dtype=torch.bfloat16, device="cuda") for T in want}
+    graphs = {}
+    for T in want:
+        graphs[T] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[T]):
+            gpu_lib.mx_moe_few(xd[:T], ld[:T], w, k, ws=ws, out=out[T])
+    for T in (64, 1, 9, 64, 2, 30, 1, 64, 9, 30, 2):
+        out[T].zero_()
+        ws.fill_(0xFF)
+        graphs[T].replay()
+        got = gpu_lib.mx_moe_few(xd[:30], ld[:30], w, k, ws=ws)
+        torch.cuda.synchronize()
+        assert same_bits(out[T], want[T]) and same_bits(got, want[30])
+
+
+def test_empty_batches(gpu_lib):
+    E, k, H, I = 6, 2, 64, 32
+    x, lg, w, *_ = few_case(gpu_lib, 3, E, k, H, I)
+    assert gpu_lib.mx_moe_few(dev_bf16(x)[:0], dev_f32(lg)[:0], w, k).shape == (0, H)
+    q = gpu_lib.mxfp4_quantize(dev_bf16(x)[:0])
+    assert q.codes.shape == (0, H // 2) and gpu_lib.mxfp4_dequantize(q).shape == (0, H)
+    zero = dev_i32(np.zeros(E + 1))
+    po = gpu_lib.mx_padded_offsets(zero)
+    assert (po == 0).all()
+    # rows, but none in a segment: nothing is written; weight gradients of empty ranges are zeros
+    c = gpu_lib.MXFP4.empty(H, gpu_lib.mx_cols_capacity(3, E))
+    c.codes.fill_(0xAA)
+    c.scales.fill_(0xAA)
+    gpu_lib.mxfp4_quantize(dev_bf16(x), layout=gpu_lib.NV4_COLS, nseg=E, seg_offsets=zero, seg_padded_offsets=po, out=c)
+    assert (c.codes == 0xAA).all() and (c.scales == 0xAA).all()
+    dw = gpu_lib.mxfp4_grouped_gemm(c, c, po, E, 0, group_mode=gpu_lib.NV4_GROUP_K)
+    assert dw.shape == (E, H, H) and (dw == 0).all()
+    y = torch.full((3, 2 * I), 7.0, device="cuda")
+    gpu_lib.mxfp4_grouped_gemm(gpu_lib.mxfp4_quantize(dev_bf16(x)), w.w13, zero, E, 2 * I, C=y)
+    assert (y == 7).all()
 
 
 def test_captured_and_replayed(gpu_lib):
