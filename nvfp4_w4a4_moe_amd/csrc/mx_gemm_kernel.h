@@ -290,15 +290,16 @@ void k_mx_gemm(MxGemmArgs g) {
       const int e = tid * per + i;
       if (e < g.E) own += (std::max(off[e + 1] - off[e], 0) + BM - 1) / BM;
     }
-    scratch[tid] = own;
-    __syncthreads();
-    for (int o = 1; o < NT; o <<= 1) {
-      const int x = tid >= o ? scratch[tid - o] : 0;
-      __syncthreads();
-      scratch[tid] += x;
-      __syncthreads();
+    int run = own;  // inclusive sum over the wave, then the waves before
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(run, o, 64);
+      if (lane >= o) run += x;
     }
-    int run = scratch[tid] - own;
+    if (lane == 63) scratch[wave] = run;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) run += scratch[w];
+    run -= own;
     for (int i = 0; i < per; ++i) {
       const int e = tid * per + i;
       if (e < g.E) {
@@ -306,7 +307,7 @@ void k_mx_gemm(MxGemmArgs g) {
         run += (std::max(off[e + 1] - off[e], 0) + BM - 1) / BM;
       }
     }
-    if (tid == NT - 1) tab[g.E] = scratch[tid];
+    if (tid == NT - 1) tab[g.E] = run;
     __syncthreads();
     constexpr int cols = SWIGLU ? BN / 2 : BN;
     tiles.ntn = (int)((g.N + cols - 1) / cols);
