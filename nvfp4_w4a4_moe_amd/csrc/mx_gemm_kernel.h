@@ -22,9 +22,16 @@
 // workgroup meets, and the slot just read is refilled: with this tile's stage s + kStages, or, in the
 // tile's last kStages stages, with the next tile's stage of that slot, so that loads run
 // across tile ends and under the epilogue.  A step's operands are read while the step before
-// multiplies, each weight fragment into the registers that the one just used leaves.  Every stage issues the same number of loads (a load with
-// nothing to fetch has an offset behind the buffer) and every epilogue the same number of
-// branch-free stores, so a wait counts exactly what may still be under way.
+// multiplies, each weight fragment into the registers that the one just used leaves.  Every stage
+// issues the same number of loads (a load with nothing to fetch has an offset behind the buffer)
+// and every epilogue the same number of branch-free stores, so a wait counts exactly what may
+// still be under way.
+//
+// Measured: 8192 x 8192 x 8192 3.4-3.8 PFLOP/s; gate and up of 131072 skewed rows of 128 experts (K
+// 2048, N 768) 295 us, 2.8 PFLOP/s, bound by the matrix cores, with a tenth of the time for the
+// SwiGLU and its stores; 768 rows of 128 experts 43 us, 5.0 TB/s of weights.  With K = 768 a tile is
+// three stages, and its stores bound it: loads return in order behind them, so the third
+// stage waits for them (FP32 weight gradients of 64 experts, 403 MB: 105 us, 70 without stores).
 #pragma once
 
 #include <algorithm>
@@ -233,8 +240,8 @@ struct MxTiles {
   }
 };
 
-// Row of B (of the tile's expert's part of it) for tile row r, or -1 behind the matrix.  SwiGLU: a wave's fragments are FN/2 of
-// gate rows, then the up rows of the same columns.
+// Row of B (of the tile's expert's part of it) for tile row r, or -1 behind the matrix.  SwiGLU: a
+// wave's fragments are FN/2 of gate rows, then the up rows of the same columns.
 template <class Cfg, int GROUP, int EPI, bool TRANS>
 __device__ __forceinline__ int mx_b_row(const MxGemmArgs &g, const MxJob &j, int r) {
   const int in = TRANS ? (r & ~31) | frag_row(r & 31) : r;

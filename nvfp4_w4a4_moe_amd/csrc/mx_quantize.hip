@@ -10,6 +10,12 @@
 // writes 256 B of codes.
 // Columns: a workgroup holds a tile of 128 rows x 256 bytes in LDS, each thread then takes
 // a 32-row block of one dword column (two BF16 columns or one FP32).
+//
+// Measured, 131072 x 2048 BF16 (537 MB in, 143 MB out per direction): rows 114 us (6.0 TB/s), columns
+// 140 (4.8), both from one read 175 (4.7), columns of rows gathered from 16384 tokens 92 (120 behind
+// other work), values back 94 (7.2).  The column form is bound by its pieces: 256 bytes of a
+// row in, 64 bytes of a column and its scale bytes out (tiles of 256 rows x 128 bytes, whole lines
+// out, were no faster).
 #include <algorithm>
 
 #include "mx_device.h"

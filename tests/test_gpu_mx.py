@@ -316,6 +316,24 @@ def test_group_k(gpu_lib, counts, N, Mc):
     assert np.array_equal(host(C16), bf16_rne_of(host(C)))
 
 
+@pytest.mark.parametrize("N,ld,first", [(96, 96, 0), (96, 98, 1), (96, 97, 0), (95, 96, 0), (95, 95, 0), (352, 360, 3),
+                                        (1, 1, 0), (2, 4, 2), (351, 352, 0)])
+@pytest.mark.parametrize("epi", [0, 1])
+@pytest.mark.parametrize("rows", [70, 900, 5000])
+def test_bf16_results_of_any_alignment(gpu_lib, N, ld, first, epi, rows):
+    """Every tile, column counts and row strides that do and do not allow stores of two columns:
+    the BF16 rows are the FP32 rows rounded, and nothing else is written."""
+    E, K = 2, 160
+    off = dev_i32(np.array([0, rows // 3, rows - 2]))
+    a = random_mx(gpu_lib, rows, K)
+    b = random_mx(gpu_lib, E * N * (1 + epi), K)
+    f32 = gpu_lib.mxfp4_grouped_gemm(a, b, off, E, N, M_cap=rows, epilogue=epi)
+    buf = torch.full((rows, ld + first), 9.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.mxfp4_grouped_gemm(a, b, off, E, N, M_cap=rows, epilogue=epi, C=buf[:, first:first + N])
+    assert same_bits(buf[:rows - 2, first:first + N].contiguous(), f32[:rows - 2].bfloat16())
+    assert (buf[:, :first] == 9).all() and (buf[:, first + N:] == 9).all() and (buf[rows - 2:] == 9).all()
+
+
 def test_many_experts_and_tiles(gpu_lib):
     """More tiles than workgroups, uneven experts, 1024 experts."""
     for E, R, K, N in ((1024, 5000, 64, 40), (16, 20000, 256, 520)):
