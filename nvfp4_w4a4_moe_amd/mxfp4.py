@@ -77,6 +77,10 @@ class MXFP4:
         return MXFP4(torch.empty((rows, K // 2), dtype=torch.uint8, device=device),
                      torch.empty((rows, mxfp4_scale_stride(K)), dtype=torch.uint8, device=device), rows, K)
 
+    def own(self) -> MXTensor:
+        """c() of a tensor that the binding has just made."""
+        return MXTensor(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.K)
+
     def c(self) -> MXTensor:
         c, s, rows, K = self.codes, self.scales, self.rows, self.K
         if not (c.dtype is s.dtype is _U8 and c.is_contiguous() and s.is_contiguous() and
@@ -194,21 +198,29 @@ def mxfp4_quantize(x: torch.Tensor, layout: int = NV4_ROWS, nseg: int = 1, seg_o
     rows, K = x.shape
     call = _Call(stream, x, seg_offsets, seg_padded_offsets, row_index, dev_status, out and out.codes,
                  out_rows and out_rows.codes)
+    ri = so = sp = ds = None
     if row_index is not None:
-        rows = row_index.numel()
-    if out is None:
+        rows, ri = row_index.numel(), _ints(row_index, "row_index")
+    if seg_offsets is not None:
+        so = _ints(seg_offsets, "seg_offsets", nseg + 1)
+    if seg_padded_offsets is not None:
+        sp = _ints(seg_padded_offsets, "seg_padded_offsets", nseg + 1)
+    if dev_status is not None:
+        ds = _ints(dev_status, "dev_status")
+    if out is not None:
+        c = out.c()
+    else:
         if layout == NV4_COLS_BATCHED:
             out = call.mx(nseg * K, rows // max(nseg, 1))
         elif layout == NV4_ROWS:
             out = call.mx(rows, K)
         else:
             out = call.mx(K, out_K if out_K is not None else mx_cols_capacity(rows, nseg))
+        c = out.own()
     if layout == NV4_ROWS_AND_COLS and out_rows is None:
         out_rows = call.mx(rows, K)
-    call(load().mxfp4_quantize, x.data_ptr(), _float(x, "x"), x.shape[0], rows, K, ldx, _ints(row_index, "row_index"),
-         layout, nseg, _ints(seg_offsets, "seg_offsets", nseg + 1),
-         _ints(seg_padded_offsets, "seg_padded_offsets", nseg + 1), rule, out.c(),
-         None if out_rows is None else out_rows.c(), _ints(dev_status, "dev_status"))
+    call(load().mxfp4_quantize, x.data_ptr(), _float(x, "x"), x.shape[0], rows, K, ldx, ri, layout, nseg, so, sp, rule,
+         c, None if out_rows is None else out_rows.c(), ds)
     if out_rows is not None:
         out.rows_out = out_rows
     return out
@@ -257,7 +269,8 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
         C = call.empty(out_dtype, *shape)
         ctype, ldc = _float(C, "C"), shape[-1]
     call(load().mxfp4_grouped_gemm, A.c(), B.c(), _ints(offsets, "offsets", E + 1), E, M_cap, N,
-         _ints(a_rows, "a_rows"), group_mode, epilogue, _p(C), ctype, ldc, None if q_out is None else q_out.c(), rule)
+         None if a_rows is None else _ints(a_rows, "a_rows"), group_mode, epilogue, _p(C), ctype, ldc,
+         None if q_out is None else q_out.c(), rule)
     return C
 
 
