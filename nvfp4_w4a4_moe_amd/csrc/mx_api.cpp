@@ -185,6 +185,7 @@ nv4_status mxfp4_grouped_gemm(const nv4_mx_tensor *A, const nv4_mx_tensor *B, co
       return fail(NV4_EINVAL, "%s: B->rows = %lld, expected E * %lld", fn, (long long)B->rows, (long long)Nb);
     if (M_cap < 0 || M_cap >= kMost32 || (!a_rows && M_cap > A->rows))
       return fail(NV4_EINVAL, "%s: M_cap exceeds the rows of A", fn);
+    if (a_rows && M_cap * 4 > most) return fail(NV4_EINVAL, "%s: too many row indices", fn);  // 32-bit offsets too
     if (a_rows && M_cap > 0 && A->rows == 0) return fail(NV4_EINVAL, "%s: row index into an empty A", fn);
     if (q_out) {
       if (epilogue != NV4_EPI_SWIGLU) return fail(NV4_EUNSUPPORTED, "%s: q_out needs the SwiGLU epilogue", fn);

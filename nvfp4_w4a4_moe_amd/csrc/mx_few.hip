@@ -35,8 +35,8 @@
 // stay: eight layers in turn, as a decode step reads them, take 42.1 us each for seven tokens
 // against 44.6; 64 tokens again and again 70 against 78, seven 39.9 against 38.2.
 //
-// Measured at H 2048, I 768, 8 of 128 experts a token: one token 14.0 us, seven 39.9 (2.9 TB/s),
-// 64 tokens 70 us (4.5 TB/s, nearly every expert's weights).
+// Measured at H 2048, I 768, 8 of 128 experts a token, weights from memory: one token 14.9 us, seven
+// 41 (2.8 TB/s), 64 tokens 75 us (4.2 TB/s, nearly every expert's weights).
 #include <algorithm>
 #include <type_traits>
 
@@ -56,8 +56,8 @@ constexpr int kMaxSplits = 4;  // workgroups that share a column tile of the dow
 constexpr uint32_t kOut = 0xFFFFFF00u;  // a byte offset behind every buffer
 
 // Workspace: per assignment f = j * T + t the expert (or -1) and its weight; the experts in use
-// with the start of their rows, and the rows' assignments; the down product's partial sums; the
-// quantised x and SwiGLU rows.
+// with the start of their rows, and the rows' tokens and weights (few_grouped); the down product's
+// partial sums; the quantised x and SwiGLU rows.
 struct FewWs {
   int32_t *id;
   float *w;
@@ -222,6 +222,7 @@ __device__ __forceinline__ i32x8 operand(u32x4 v) {  // FP4 reads the first four
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
+
 // ---------------------------------------------------------------- 2. gate and up
 
 constexpr int kGuWaves = 8, kGuSteps = 2;  // steps of K = 128 a wave holds at a time
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_group(MxFewArgs a) {
   }
 }
 
-// FUSED (logits given, T <= kFusedTokens, T * H <= kFusedElems): routes and quantises x as well;
+// FUSED (few_fused): routes and quantises x as well;
 // NPL, LPT as for topk_token, F32 the type of x.
 template <bool FUSED, int NPL, int LPT, bool F32>
 __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {

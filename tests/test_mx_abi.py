@@ -133,6 +133,7 @@ def test_sizes_behind_32_bit_offsets_are_refused(lib):
     n = 1 << 22
     assert _gemm(lib, E=1, N=n, ldc=n, M=1, A=mx(100, 2112), B=mx(n, 2112)) == EINVAL  # one expert above 4 GiB
     assert b"4 GiB" in lib.nv4_last_error()
+    assert _gemm(lib, ri=P, M=1 << 30) == EINVAL and b"row indices" in lib.nv4_last_error()
     seg = dict(layout=2, so=P, sp=P, out=mx(96, 256))
     assert _quantize(lib, ldx=n + 8, **seg) == EINVAL and b"2^22" in lib.nv4_last_error()
     assert _quantize(lib, ldx=n + 8, layout=3, nseg=2, out=mx(192, 32)) == EINVAL
