@@ -13,11 +13,8 @@
 //                     for all the expert's tokens, SwiGLU and re-quantisation: 32 columns are
 //                     one MX block.  The K dimension is split over the eight waves.  Every wave
 //                     finds its expert's rows itself from the T * k ids (ballots, no sorting).
-//      With more than kGroupedRows assignments (few_grouped) k_few_group and the grouped GEMM
-//                     (mx_gemm_kernel.h) take its place: the first lists the experts in use and
-//                     their rows.  Its 5 us pay once the GEMM's rows come cheaper (8 of 128
-//                     experts a token: 9 tokens 42.5 us here, 47.0 grouped; 14 tokens 52.4 and
-//                     50.6).
+//      With more assignments (few_grouped) k_few_group and the grouped GEMM (mx_gemm_kernel.h) take
+//                     its place: the first lists the experts in use and their rows.
 //   3. k_few_down     one workgroup per 16 columns of H: its waves walk over the assignments
 //                     (few_grouped: the experts in use), add weight * product into a token table
 //                     in LDS (one per wave), and the tables are summed in wave order.  Where there
@@ -229,9 +226,8 @@ constexpr int kGuWaves = 8, kGuSteps = 2;  // steps of K = 128 a wave holds at a
 constexpr int kGuThreads = kGuWaves * 64;
 constexpr int kGuCodes = 64 * kGuSteps * 64, kGuSlot = kGuCodes + 64 * kGuSteps * 4;
 
-// Batches with more assignments than this go through the grouped GEMM (see the top).
-constexpr int kGroupedRows = 72;
-constexpr int kIdChunks = (kGroupedRows + 63) / 64;
+constexpr int kMostRows = 128;  // assignments without few_grouped
+constexpr int kIdChunks = kMostRows / 64;
 constexpr int kFusedElems = 8192;                // tokens x H that a workgroup quantises for itself
 constexpr int kFusedTokens = 2;
 
@@ -699,7 +695,16 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   }
 }
 
-bool few_grouped(const MxFewArgs &a) { return a.T * a.k > kGroupedRows; }
+// Listing the experts costs 5 us, which pay once experts have several rows each: the GEMM, and the
+// down product by experts, then read their weights once.  Measured in us, layers in turn, one by
+// one / grouped, by assignments:
+//   8 experts (H 4096, I 1536)    16 31.4 / 31.0   32 39.5 / 39.0   48 47.4 / 39.4   64 54.8 / 39.1
+//   64 (H 2048, I 1024)           48 44.4 / 51.2   72 51.4 / 52.9   96 58.8 / 55.2
+//   128 (H 2048, I 768)           72 47.2 / 51.1   80 49.7 / 51.7   96 54.2 / 54.3  112 58.7 / 55.0
+//   256 (H 2048, I 512)           64 39.2 / 42.8   96 49.0 / 55.1  128 58.1 / 59.6
+bool few_grouped(const MxFewArgs &a) {
+  return a.T * a.k > std::min({4 * a.E, 64 + a.E / 4, kMostRows});
+}
 
 // The smallest batches: one kernel less (see the top).
 bool few_fused(const MxFewArgs &a) {

@@ -587,6 +587,13 @@ def test_few_many_rows_and_windows(gpu_lib, T, E, k, H, I):
     test_few(gpu_lib, T, E, k, H, I)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (12, 260, 8, 64, 32), (16, 300, 8, 96, 64), (64, 256, 2, 64, 32), (13, 128, 8, 64, 32), (12, 128, 8, 64, 32),
+    (16, 8, 2, 64, 96), (17, 8, 2, 64, 96), (2, 600, 32, 64, 32), (4, 1024, 32, 64, 32)])
+def test_few_on_either_side_of_its_rule(gpu_lib, T, E, k, H, I):
+    test_few(gpu_lib, T, E, k, H, I)
+
+
 def random_mx(gpu_lib, rows, K):
     """Random codes under scales 2^-7 .. 1, made on the GPU."""
     codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda")
