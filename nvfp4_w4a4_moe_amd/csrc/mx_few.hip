@@ -695,20 +695,24 @@ __global__ __launch_bounds__(kDnWaves * 64) void k_few_down(MxFewArgs a, int spl
   }
 }
 
-// Listing the experts costs 5 us, which pay once experts have several rows each: the GEMM, and the
-// down product by experts, then read their weights once.  Measured in us, layers in turn, one by
-// one / grouped, by assignments:
-//   8 experts (H 4096, I 1536)    16 31.4 / 31.0   32 39.5 / 39.0   48 47.4 / 39.4   64 54.8 / 39.1
-//   64 (H 2048, I 1024)           48 44.4 / 51.2   72 51.4 / 52.9   96 58.8 / 55.2
-//   128 (H 2048, I 768)           72 47.2 / 51.1   80 49.7 / 51.7   96 54.2 / 54.3  112 58.7 / 55.0
-//   256 (H 2048, I 512)           64 39.2 / 42.8   96 49.0 / 55.1  128 58.1 / 59.6
-bool few_grouped(const MxFewArgs &a) {
-  return a.T * a.k > std::min({4 * a.E, 64 + a.E / 4, kMostRows});
-}
+// The smallest batches: one kernel less (see the top) when they are routed here.
+bool few_smallest(const MxFewArgs &a) { return a.T <= kFusedTokens && (int64_t)a.T * a.H <= kFusedElems; }
+bool few_fused(const MxFewArgs &a) { return a.logits && few_smallest(a); }
 
-// The smallest batches: one kernel less (see the top).
-bool few_fused(const MxFewArgs &a) {
-  return a.logits && a.T <= kFusedTokens && (int64_t)a.T * a.H <= kFusedElems;
+// Listing the experts costs 5 us, which pay once experts have several rows each: the GEMM, and the
+// down product by experts, then read their weights once.  (Not the smallest batches: the same routing
+// has the same bits whether it is computed here or given.)  Measured in us, layers in turn, one by
+// one / grouped, by assignments:
+//   8 experts (H 4096, I 14336)    8  106 / 113   12  143 / 130   16  163 / 141   32  240 / 151
+//   8 (H 4096, I 1536)            16 31.4 / 31.0  32 39.5 / 39.0  48 47.4 / 39.4
+//   16 (H 4096, I 4096)           16 70.2 / 77.6  24 86.3 / 88.2  32 99.7 / 88.7
+//   32 (H 2880, I 2880)           24 74.6 / 79.8  40  102 / 100   64  135 / 117
+//   64 (H 2048, I 1408)           48 51.5 / 53.5  60 58.8 / 55.7  96 71.9 / 66.8
+//   64 (H 2048, I 1024)           48 44.4 / 51.2  72 51.4 / 52.9  96 58.8 / 55.2
+//   128 (H 2048, I 768)           72 47.2 / 51.1  96 54.2 / 54.3 112 58.7 / 55.0
+//   256 (H 2048, I 512)           64 39.2 / 42.8  96 49.0 / 55.1 128 58.1 / 59.6
+bool few_grouped(const MxFewArgs &a) {
+  return !few_smallest(a) && a.T * a.k > std::min({a.E + 4, 64 + a.E / 4, kMostRows});
 }
 
 template <int NPL, int LPT, bool F32>
