@@ -102,11 +102,16 @@ def _float(t: torch.Tensor, name: str) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str) -> int:
-    """The row stride of a 2-D tensor with contiguous rows."""
+    """The row stride of a 2-D tensor with contiguous rows (the width where there is one row at
+    most, whose stride means nothing)."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return max(stride[0], shape[1])
+    if shape[0] <= 1:
+        return shape[1]
+    if stride[0] < shape[1]:
+        raise ValueError(f"{name} has rows that overlap (row stride {stride[0]}, width {shape[1]})")
+    return stride[0]
 
 
 def _ints(t: torch.Tensor | None, name: str, n: int | None = None):
@@ -264,7 +269,7 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
         if C.dim() != len(shape) or C.stride(-1) != 1 and C.shape[-1] > 1 or C.shape[-2] < shape[-2] or \
                 C.shape[-1] != shape[-1] or group_mode == NV4_GROUP_K and (C.shape[0] != E or not C.is_contiguous()):
             raise ValueError(f"C must be {list(shape)} with contiguous rows")
-        ldc = max(C.stride(-2), C.shape[-1])
+        ldc = shape[-1] if group_mode == NV4_GROUP_K else _matrix(C, "C")
     elif want_c:
         C = call.empty(out_dtype, *shape)
         ctype, ldc = _float(C, "C"), shape[-1]

@@ -1,0 +1,158 @@
+"""The MXFP4 binding on the CPU: what it passes to the library, on which stream, and what it
+refuses.  A stand-in library records every call; tensors say that they are on a GPU, but live in
+host memory, and streams are names.  No kernel runs, so a wrong stride, buffer or stream shows
+here without touching memory that is not the call's."""
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+import nvfp4_w4a4_moe_amd as nv4
+from nvfp4_w4a4_moe_amd import mxfp4
+
+BF16 = torch.bfloat16
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on GPU 0."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, stream):
+        Gpu.now.recorded.setdefault(self.data_ptr(), set()).add(stream.cuda_stream)
+
+
+class Stream:
+    def __init__(self, name, device="cpu"):
+        self.cuda_stream, self.device = name, torch.device(device)
+
+    def __eq__(self, other):
+        return self.cuda_stream == other.cuda_stream
+
+    def __hash__(self):
+        return hash(self.cuda_stream)
+
+    def record_event(self, event=None):
+        return event
+
+
+class Gpu:
+    """The stand-in: `calls` holds (function, arguments, the stream it was given, the current device),
+    `made` the stream on which each tensor was allocated or copied, by address."""
+    now = None
+
+    def __init__(self, monkeypatch):
+        Gpu.now = self
+        self.calls, self.made, self.recorded, self.device = [], {}, {}, 0
+        self.keep = []   # (no address is used twice)
+        self.stream = Stream(100)
+        empty, reshape = torch.empty, torch.Tensor.reshape
+
+        def on_gpu(*shape, device=None, **k):
+            t = empty(*shape, **k).as_subclass(OnGpu)
+            self.made[t.data_ptr()] = self.stream.cuda_stream
+            self.keep.append(t)
+            return t
+
+        @contextlib.contextmanager
+        def stream(s):
+            old, self.stream = self.stream, s
+            dev, self.device = self.device, 0
+            yield
+            self.stream, self.device = old, dev
+
+        @contextlib.contextmanager
+        def device(d):
+            old, self.device = self.device, 0 if isinstance(d, torch.device) else d
+            yield
+            self.device = old
+
+        def copied(t, *shape):
+            r = reshape(t, *shape)
+            if r.data_ptr() != t.data_ptr():
+                self.made[r.data_ptr()] = self.stream.cuda_stream
+                self.keep.append(r)
+            return r
+
+        monkeypatch.setattr(torch, "empty", on_gpu)
+        monkeypatch.setattr(OnGpu, "reshape", copied, raising=False)
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.device)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: self.stream)
+        monkeypatch.setattr(mxfp4, "_raw_stream", lambda i: self.stream.cuda_stream)
+        monkeypatch.setattr(mxfp4, "load", lambda: self)
+        monkeypatch.setattr(nv4, "load", lambda: self)
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace"):
+            return lambda *a: 4096
+        return lambda *a: self.calls.append((name, a[:-1], getattr(a[-1], "value", a[-1]), self.device)) or 0
+
+    def args(self, name):
+        return [a for n, a, *_ in self.calls if n == name]
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    g = Gpu(monkeypatch)
+    yield g
+    Gpu.now = None
+
+
+def ten(*shape, dtype=BF16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def mx(rows, K):
+    u8 = torch.uint8
+    return nv4.MXFP4(ten(rows, K // 2, dtype=u8), ten(rows, nv4.mxfp4_scale_stride(K), dtype=u8), rows, K)
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32).as_subclass(OnGpu)
+
+
+def weights(E, H, I):
+    return nv4.MXExpertWeights(mx(E * 2 * I, H), mx(E * H, I), E, H, I)
+
+
+# ----------------------------------------------------------------------------- strides
+
+# rows that overlap: one row repeated, and windows that share half of their elements
+OVERLAPPING = [lambda n, dt: ten(1, 64, dtype=dt).expand(n, 64),
+               lambda n, dt: ten((n + 1) * 32, dtype=dt).unfold(0, 64, 32)]
+
+
+@pytest.mark.parametrize("make", OVERLAPPING)
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_rows_that_overlap_are_refused(gpu, make, dtype):
+    """The library takes a matrix by its row stride.  A stride below the width is refused and
+    never replaced by the width, which reads or writes rows that are not there."""
+    w, lg, ok = weights(4, 64, 32), ten(3, 4, dtype=torch.float32), ten(3, 64, dtype=dtype)
+    bad = make(3, dtype)
+    for call in (lambda: nv4.mxfp4_quantize(bad),
+                 lambda: nv4.mxfp4_quantize(bad, row_index=i32(0, 1, 2, 2)),
+                 lambda: nv4.mxfp4_dequantize(mx(3, 64), out=bad),
+                 lambda: nv4.mx_moe_few(bad, lg, w, 2),
+                 lambda: nv4.mx_moe_few(ok, lg, w, 2, out=bad),
+                 lambda: nv4.mxfp4_grouped_gemm(mx(3, 96), mx(64, 96), i32(0, 3), 1, 64, C=bad)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert not gpu.calls
+
+
+def test_row_strides_are_the_tensors(gpu):
+    wide = ten(5, 96)
+    for x, ldx in ((wide, 96), (wide[:, :64], 96), (wide[::2, 32:], 192), (wide[:1, :64], 64), (ten(64).expand(1, 64), 64),
+                   (ten(96, 1).t()[:, :64], 64)):
+        nv4.mxfp4_quantize(x)
+        assert gpu.args("mxfp4_quantize")[-1][5] == ldx
+        nv4.mxfp4_dequantize(mx(*x.shape), out=x)
+        assert gpu.args("mxfp4_dequantize")[-1][3] == ldx
+        nv4.mxfp4_grouped_gemm(mx(x.shape[0], 96), mx(x.shape[1], 96), i32(0, 1), 1, x.shape[1], C=x)
+        assert gpu.args("mxfp4_grouped_gemm")[-1][11] == ldx
