@@ -266,10 +266,14 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
     ldc, ctype = 0, NV4_F32
     if C is not None:
         ctype = _float(C, "C")
-        if C.dim() != len(shape) or C.stride(-1) != 1 and C.shape[-1] > 1 or C.shape[-2] < shape[-2] or \
-                C.shape[-1] != shape[-1] or group_mode == NV4_GROUP_K and (C.shape[0] != E or not C.is_contiguous()):
-            raise ValueError(f"C must be {list(shape)} with contiguous rows")
-        ldc = shape[-1] if group_mode == NV4_GROUP_K else _matrix(C, "C")
+        if group_mode == NV4_GROUP_K:
+            if C.shape != shape or not C.is_contiguous():
+                raise ValueError(f"C must be {list(shape)} and contiguous")
+            ldc = shape[-1]
+        else:
+            if C.dim() != 2 or C.shape[0] < M_cap or C.shape[1] != N:
+                raise ValueError(f"C must be {list(shape)} with contiguous rows")
+            ldc = _matrix(C, "C")
     elif want_c:
         C = call.empty(out_dtype, *shape)
         ctype, ldc = _float(C, "C"), shape[-1]

@@ -156,3 +156,15 @@ def test_row_strides_are_the_tensors(gpu):
         assert gpu.args("mxfp4_dequantize")[-1][3] == ldx
         nv4.mxfp4_grouped_gemm(mx(x.shape[0], 96), mx(x.shape[1], 96), i32(0, 1), 1, x.shape[1], C=x)
         assert gpu.args("mxfp4_grouped_gemm")[-1][11] == ldx
+
+
+@pytest.mark.parametrize("shape", [(2, 9, 64), (2, 7, 64), (2, 8, 65), (3, 8, 64), (16, 64)])
+def test_weight_gradients_have_their_own_shape(gpu, shape):
+    """Expert e's part of C starts e * A.rows rows in: a C with more rows would get them displaced."""
+    o = dict(group_mode=nv4.NV4_GROUP_K)
+    a, b, off = mx(8, 128), mx(64, 128), i32(0, 128, 128)
+    with pytest.raises(ValueError, match=r"C must be \[2, 8, 64\]"):
+        nv4.mxfp4_grouped_gemm(a, b, off, 2, 0, C=ten(*shape), **o)
+    assert not gpu.calls
+    assert nv4.mxfp4_grouped_gemm(a, b, off, 2, 0, C=ten(2, 8, 64), **o).shape == (2, 8, 64)
+    assert gpu.args("mxfp4_grouped_gemm")[-1][11] == 64
