@@ -202,7 +202,7 @@ def mxfp4_quantize(x: torch.Tensor, layout: int = NV4_ROWS, nseg: int = 1, seg_o
     ldx = _matrix(x, "x")
     rows, K = x.shape
     call = _Call(stream, x, seg_offsets, seg_padded_offsets, row_index, dev_status, out and out.codes,
-                 out_rows and out_rows.codes)
+                 out and out.scales, out_rows and out_rows.codes, out_rows and out_rows.scales)
     ri = so = sp = ds = None
     if row_index is not None:
         rows, ri = row_index.numel(), _ints(row_index, "row_index")
@@ -254,7 +254,8 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
     """GROUP_M: C [M_cap, N] = per-expert A_e . B_e^T (SwiGLU: N output columns from 2N rows of
     B per expert).  GROUP_K: C [E, A.rows, B.rows] over per-expert K ranges.  q_out (SwiGLU):
     also the MXFP4 form of the result; with want_c=False that alone."""
-    call = _Call(stream, A.codes, A.scales, B.codes, B.scales, offsets, a_rows, C, q_out and q_out.codes)
+    call = _Call(stream, A.codes, A.scales, B.codes, B.scales, offsets, a_rows, C, q_out and q_out.codes,
+                 q_out and q_out.scales)
     if group_mode == NV4_GROUP_K:
         M_cap, N, shape = 0, A.rows, (E, A.rows, B.rows)
     else:

@@ -168,3 +168,20 @@ def test_weight_gradients_have_their_own_shape(gpu, shape):
     assert not gpu.calls
     assert nv4.mxfp4_grouped_gemm(a, b, off, 2, 0, C=ten(2, 8, 64), **o).shape == (2, 8, 64)
     assert gpu.args("mxfp4_grouped_gemm")[-1][11] == 64
+
+
+# ----------------------------------------------------------------------------- devices
+
+def test_scales_on_another_device_are_refused(gpu):
+    """A tensor's codes and scales are both written or read by the kernel: both have to be there."""
+    half = lambda rows, K: nv4.MXFP4(mx(rows, K).codes, torch.zeros(rows, nv4.mxfp4_scale_stride(K), dtype=torch.uint8),
+                                     rows, K)
+    x, seg = ten(4, 64), dict(nseg=1, seg_offsets=i32(0, 4), seg_padded_offsets=i32(0, 128))
+    for call in (lambda: nv4.mxfp4_quantize(x, out=half(4, 64)),
+                 lambda: nv4.mxfp4_quantize(x, layout=nv4.NV4_ROWS_AND_COLS, out=mx(64, 256), out_rows=half(4, 64), **seg),
+                 lambda: nv4.mxfp4_dequantize(half(4, 64)),
+                 lambda: nv4.mxfp4_grouped_gemm(mx(4, 64), mx(64, 64), i32(0, 4), 1, 32, epilogue=nv4.NV4_EPI_SWIGLU,
+                                                q_out=half(4, 32), want_c=False)):
+        with pytest.raises(ValueError, match="tensors on"):
+            call()
+    assert not gpu.calls
