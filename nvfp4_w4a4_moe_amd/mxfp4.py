@@ -127,9 +127,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 
 
 class _Call:
-    """One call's device and stream: every tensor has to be on the device of the first one, the
-    launch goes to the given stream or to that device's current one, and temporaries stay
-    alive for that stream."""
+    """One call's device and stream: every tensor has to be on the device of the first one, and the
+    launch goes to the given stream or to that device's current one.  Memory comes from the pool
+    of that stream: a block of the current stream's pool may still be in use by kernels queued
+    there, which another stream does not wait for."""
 
     __slots__ = ("index", "device", "given", "stream")
 
@@ -143,13 +144,23 @@ class _Call:
             raise ValueError(f"tensors must be on a GPU, not on {first.device}")
         if stream is not None and stream.device != self.device:
             raise ValueError(f"stream of {stream.device} for tensors on {self.device}")
-        self.index, self.given = index, stream
-        self.stream = _raw_stream(index) if stream is None else stream.cuda_stream
+        self.index, self.given = index, None
+        self.stream = _raw_stream(index)
+        if stream is not None and stream.cuda_stream != self.stream:
+            self.given, self.stream = stream, stream.cuda_stream
+
+    def scratch(self, dtype, *shape) -> torch.Tensor:
+        """Memory that the call alone uses: free for the stream's next work when the call returns."""
+        if self.given is None:
+            return torch.empty(*shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.given):
+            return torch.empty(*shape, dtype=dtype, device=self.device)
 
     def empty(self, dtype, *shape) -> torch.Tensor:
-        t = torch.empty(*shape, dtype=dtype, device=self.device)
+        """An output: the caller's stream, where it is read next, keeps it from reuse as well."""
+        t = self.scratch(dtype, *shape)
         if self.given is not None:
-            t.record_stream(self.given)
+            t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def mx(self, rows: int, K: int) -> MXFP4:
@@ -462,7 +473,7 @@ def mx_moe_few(x: torch.Tensor, logits: torch.Tensor | None, w: MXExpertWeights,
     elif out.shape != x.shape:
         raise ValueError(f"out must be [{T}, {H}]")
     if ws is None:
-        ws = call.empty(_U8, max(_few_workspace(T, w.E, k, H, w.I), 256))
+        ws = call.scratch(_U8, max(_few_workspace(T, w.E, k, H, w.I), 256))
     elif ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be contiguous uint8")
     call(load().mx_moe_few, x.data_ptr(), _float(x, "x"), ldx, _p(logits), T, w.E, k, flags,

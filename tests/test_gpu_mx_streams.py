@@ -1,0 +1,62 @@
+"""MXFP4 calls on a stream of their own while the current one is busy: where their memory comes
+from, and that neither stream's results change."""
+
+import pytest
+import torch
+
+from tests.gpu_util import same_bits
+from tests.test_gpu_mx import dev_bf16, dev_f32, few_case
+
+pytestmark = pytest.mark.gpu
+
+
+def pool_of(t):
+    """The stream whose pool holds t's memory."""
+    p = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= p < s["address"] + s["total_size"])
+
+
+def keep_busy(n=20):
+    """Some milliseconds of work for the current stream, so that what is queued behind it is still
+    pending when the host goes on."""
+    a = torch.ones(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    for _ in range(n):
+        torch.mm(a, a)
+
+
+def test_outputs_come_from_the_streams_pool(gpu_lib):
+    T, E, k, H, I = 12, 16, 4, 256, 64
+    x, lg, w, *_ = few_case(gpu_lib, T, E, k, H, I)
+    x, lg, s = dev_bf16(x), dev_f32(lg), torch.cuda.Stream()
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    q = gpu_lib.mxfp4_quantize(x, stream=s)
+    outs = [q.codes, q.scales, gpu_lib.mxfp4_dequantize(q, stream=s), gpu_lib.mx_padded_offsets(off, stream=s),
+            gpu_lib.mxfp4_grouped_gemm(q, w.w13, off, 1, E * 2 * I, stream=s),
+            gpu_lib.mx_moe_few(x, lg, w, k, stream=s)]
+    assert [pool_of(t) for t in outs] == [s.cuda_stream] * len(outs)
+    assert pool_of(x) != s.cuda_stream
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_a_call_behind_a_busy_stream_and_one_beside_it(gpu_lib, T):
+    """Without ws: the first call's workspace is free for the current stream again when the call
+    returns, with its kernels still pending.  The second must not get it."""
+    E, k, H, I = 16, 4, 1024, 256
+    x, lg, w, *_ = few_case(gpu_lib, 2 * T, E, k, H, I)
+    x, lg = dev_bf16(x), dev_f32(lg)
+    a, b = (x[:T], lg[:T]), (x[T:], lg[T:])
+    want = gpu_lib.mx_moe_few(*a, w, k), gpu_lib.mx_moe_few(*b, w, k)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        keep_busy()
+        outs.append((gpu_lib.mx_moe_few(*a, w, k), want[0]))
+        for _ in range(3):
+            outs.append((gpu_lib.mx_moe_few(*b, w, k, stream=s), want[1]))
+        outs.append((gpu_lib.mx_moe_few(*a, w, k), want[0]))
+    torch.cuda.synchronize()
+    for got, ref in outs:
+        assert same_bits(got, ref)

@@ -185,3 +185,42 @@ def test_scales_on_another_device_are_refused(gpu):
         with pytest.raises(ValueError, match="tensors on"):
             call()
     assert not gpu.calls
+
+
+# ----------------------------------------------------------------------------- streams
+
+def single_calls(stream):
+    """Each call that makes its own outputs or workspace, as (call, its tensors)."""
+    x, w, off, lg = ten(3, 64), weights(4, 64, 32), i32(0, 3), ten(3, 4, dtype=torch.float32)
+    o = dict(stream=stream)
+    both = dict(layout=nv4.NV4_ROWS_AND_COLS, seg_offsets=off, seg_padded_offsets=i32(0, 128))
+    pair = lambda q: [q.codes, q.scales]
+    return [lambda: pair(nv4.mxfp4_quantize(x, **o)),
+            lambda: sum(map(pair, (lambda q: (q, q.rows_out))(nv4.mxfp4_quantize(x, **both, **o))), []),
+            lambda: [nv4.mxfp4_dequantize(mx(3, 64), **o)], lambda: [nv4.mx_padded_offsets(off, **o)],
+            lambda: [nv4.mxfp4_grouped_gemm(mx(3, 64), mx(32, 64), off, 1, 32, **o)],
+            lambda: [nv4.mx_moe_few(x, lg, w, 2, **o)]]
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_a_streams_call_takes_the_streams_memory(gpu, i):
+    """A block of the current stream's pool may still be in use by kernels queued there, for which a
+    call on another stream does not wait.  So outputs and workspaces come from the pool of the
+    stream that writes them, and the outputs are kept from reuse until the caller's stream is done
+    with them."""
+    call = single_calls(Stream(200))[i]
+    gpu.made.clear()
+    outs = call()
+    assert gpu.calls and {s for *_, s, _ in gpu.calls} == {200}
+    assert gpu.made and set(gpu.made.values()) == {200}
+    assert {t.data_ptr() for t in outs} == {a for a, s in gpu.recorded.items() if s == {100}} == set(gpu.recorded)
+    assert gpu.stream == Stream(100)
+
+
+@pytest.mark.parametrize("i", range(6))
+@pytest.mark.parametrize("given", [None, 100])
+def test_the_current_streams_call_stays_there(gpu, i, given):
+    call = single_calls(given and Stream(given))[i]
+    gpu.made.clear()
+    call()
+    assert {s for *_, s, _ in gpu.calls} == {100} == set(gpu.made.values()) and not gpu.recorded
