@@ -15,6 +15,7 @@ package's top level.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 from dataclasses import dataclass
@@ -297,6 +298,38 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
 
 # ----------------------------------------------------------------------------- layer composition
 
+class _Layer:
+    """Makes the given stream current while a layer's calls are queued on it, so that what they
+    allocate comes from its pool (as for one call, see _Call)."""
+
+    def __init__(self, stream, x: torch.Tensor):
+        if not x.is_cuda:
+            raise ValueError(f"tensors must be on a GPU, not on {x.device}")
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {x.device}")
+        self.caller = torch.cuda.current_stream(x.device)
+        self.on = contextlib.nullcontext() if stream is None or stream == self.caller else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.on.__enter__()
+        self.stream = torch.cuda.current_stream()
+        return self
+
+    def __exit__(self, *exc):
+        return self.on.__exit__(*exc)
+
+    def made(self, bufs):
+        """`bufs`, which the layer has allocated and returns: the caller's stream keeps their tensors
+        from reuse as well."""
+        if self.stream != self.caller:
+            for v in vars(bufs).values():
+                if isinstance(v, torch.Tensor):
+                    v.record_stream(self.caller)
+                elif isinstance(v, MXFP4):
+                    self.made(v)
+        return bufs
+
+
 @dataclass
 class MXExpertWeights:
     """Quantised expert weights: W13 [E*2I, H] (per expert gate rows, then up rows), W2 [E*H, I]."""
@@ -363,23 +396,23 @@ def mx_moe_forward(x: torch.Tensor, logits: torch.Tensor, w: MXExpertWeights, k:
     """One MXFP4 expert-layer forward: quantise x, route and permute, gate and up products with
     SwiGLU and re-quantisation in the epilogue, down product, combine (``out``)."""
     T, H = x.shape
-    if bufs is None:
-        bufs = mx_alloc_forward(T, H, w.E, k, w.I, device=x.device)
     R = T * k
-    st = stream if stream is not None else torch.cuda.current_stream()
-    with _Stage(stage_events, "quantize_x", st):
-        mxfp4_quantize(x, out=bufs.xq, rule=bufs.rule, stream=stream)
-    with _Stage(stage_events, "route_permute", st):
-        bufs.routing = moe_permute(logits, w.E, k, flags=flags, ws=bufs.pws, stream=stream, out=bufs.routing)
-    rt = bufs.routing
-    with _Stage(stage_events, "gemm1_swiglu", st):
-        mxfp4_grouped_gemm(bufs.xq, w.w13, rt.offsets, w.E, w.I, M_cap=R, a_rows=rt.row_token,
-                           epilogue=NV4_EPI_SWIGLU, C=bufs.hact, want_c=False, q_out=bufs.hq, rule=bufs.rule,
-                           stream=stream)
-    with _Stage(stage_events, "gemm2", st):
-        mxfp4_grouped_gemm(bufs.hq, w.w2, rt.offsets, w.E, H, M_cap=R, C=bufs.y, stream=stream)
-    with _Stage(stage_events, "combine", st):
-        moe_combine(bufs.y, rt.token_row, rt.topk_w, out=bufs.out, stream=stream)
+    with _Layer(stream, x) as layer:
+        st = layer.stream
+        if bufs is None:
+            bufs = layer.made(mx_alloc_forward(T, H, w.E, k, w.I, device=x.device))
+        with _Stage(stage_events, "quantize_x", st):
+            mxfp4_quantize(x, out=bufs.xq, rule=bufs.rule)
+        with _Stage(stage_events, "route_permute", st):
+            rt = moe_permute(logits, w.E, k, flags=flags, ws=bufs.pws, out=bufs.routing)
+            bufs.routing = layer.made(rt) if bufs.routing is None else rt
+        with _Stage(stage_events, "gemm1_swiglu", st):
+            mxfp4_grouped_gemm(bufs.xq, w.w13, rt.offsets, w.E, w.I, M_cap=R, a_rows=rt.row_token,
+                               epilogue=NV4_EPI_SWIGLU, C=bufs.hact, want_c=False, q_out=bufs.hq, rule=bufs.rule)
+        with _Stage(stage_events, "gemm2", st):
+            mxfp4_grouped_gemm(bufs.hq, w.w2, rt.offsets, w.E, H, M_cap=R, C=bufs.y)
+        with _Stage(stage_events, "combine", st):
+            moe_combine(bufs.y, rt.token_row, rt.topk_w, out=bufs.out)
     return bufs
 
 
@@ -423,28 +456,28 @@ def mx_moe_backward(x: torch.Tensor, fwd: MXForwardBuffers, wt: MXTransposedWeig
     T, H = x.shape
     rt = fwd.routing
     E, R, I = rt.offsets.numel() - 1, rt.row_token.numel(), fwd.hact.shape[1]
-    if bufs is None:
-        bufs = mx_alloc_backward(T, H, E, R // T, I, device=x.device)
-    st = stream if stream is not None else torch.cuda.current_stream()
-    seg = dict(nseg=E, seg_offsets=rt.offsets, seg_padded_offsets=bufs.padded, rule=fwd.rule, stream=stream)
-    with _Stage(stage_events, "quantize_dy2", st):
-        mx_padded_offsets(rt.offsets, out=bufs.padded, stream=stream)
-        mxfp4_quantize(dY2, layout=NV4_ROWS_AND_COLS, out=bufs.dy2c, out_rows=bufs.dy2q, **seg)
-    with _Stage(stage_events, "quantize_dy13", st):
-        mxfp4_quantize(dY13, layout=NV4_ROWS_AND_COLS, out=bufs.dy13c, out_rows=bufs.dy13q, **seg)
-    with _Stage(stage_events, "dgrad_hact", st):
-        mxfp4_grouped_gemm(bufs.dy2q, wt.w2t, rt.offsets, E, I, M_cap=R, C=bufs.dhact, stream=stream)
-    with _Stage(stage_events, "dgrad_x", st):
-        mxfp4_grouped_gemm(bufs.dy13q, wt.w13t, rt.offsets, E, H, M_cap=R, C=bufs.dxperm, stream=stream)
-    with _Stage(stage_events, "quantize_cols_hact", st):
-        mxfp4_quantize(fwd.hact, layout=NV4_COLS, out=bufs.hc, **seg)
-    with _Stage(stage_events, "wgrad_w2", st):
-        mxfp4_grouped_gemm(bufs.dy2c, bufs.hc, bufs.padded, E, H, group_mode=NV4_GROUP_K, C=bufs.dw2, stream=stream)
-    with _Stage(stage_events, "quantize_cols_x", st):
-        mxfp4_quantize(x, layout=NV4_COLS, out=bufs.xc, row_index=rt.row_token, **seg)
-    with _Stage(stage_events, "wgrad_w13", st):
-        mxfp4_grouped_gemm(bufs.dy13c, bufs.xc, bufs.padded, E, 2 * I, group_mode=NV4_GROUP_K, C=bufs.dw13,
-                           stream=stream)
+    with _Layer(stream, x) as layer:
+        st = layer.stream
+        if bufs is None:
+            bufs = layer.made(mx_alloc_backward(T, H, E, R // T, I, device=x.device))
+        seg = dict(nseg=E, seg_offsets=rt.offsets, seg_padded_offsets=bufs.padded, rule=fwd.rule)
+        with _Stage(stage_events, "quantize_dy2", st):
+            mx_padded_offsets(rt.offsets, out=bufs.padded)
+            mxfp4_quantize(dY2, layout=NV4_ROWS_AND_COLS, out=bufs.dy2c, out_rows=bufs.dy2q, **seg)
+        with _Stage(stage_events, "quantize_dy13", st):
+            mxfp4_quantize(dY13, layout=NV4_ROWS_AND_COLS, out=bufs.dy13c, out_rows=bufs.dy13q, **seg)
+        with _Stage(stage_events, "dgrad_hact", st):
+            mxfp4_grouped_gemm(bufs.dy2q, wt.w2t, rt.offsets, E, I, M_cap=R, C=bufs.dhact)
+        with _Stage(stage_events, "dgrad_x", st):
+            mxfp4_grouped_gemm(bufs.dy13q, wt.w13t, rt.offsets, E, H, M_cap=R, C=bufs.dxperm)
+        with _Stage(stage_events, "quantize_cols_hact", st):
+            mxfp4_quantize(fwd.hact, layout=NV4_COLS, out=bufs.hc, **seg)
+        with _Stage(stage_events, "wgrad_w2", st):
+            mxfp4_grouped_gemm(bufs.dy2c, bufs.hc, bufs.padded, E, H, group_mode=NV4_GROUP_K, C=bufs.dw2)
+        with _Stage(stage_events, "quantize_cols_x", st):
+            mxfp4_quantize(x, layout=NV4_COLS, out=bufs.xc, row_index=rt.row_token, **seg)
+        with _Stage(stage_events, "wgrad_w13", st):
+            mxfp4_grouped_gemm(bufs.dy13c, bufs.xc, bufs.padded, E, 2 * I, group_mode=NV4_GROUP_K, C=bufs.dw13)
     return bufs
 
 

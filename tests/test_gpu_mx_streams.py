@@ -60,3 +60,41 @@ def test_a_call_behind_a_busy_stream_and_one_beside_it(gpu_lib, T):
     torch.cuda.synchronize()
     for got, ref in outs:
         assert same_bits(got, ref)
+
+
+def layer_case(gpu_lib, T=96, E=8, k=2, H=256, I=64):
+    x, lg, w, v13, v2 = few_case(gpu_lib, T, E, k, H, I)
+    g = torch.Generator("cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, dtype=torch.bfloat16, device="cuda", generator=g)
+    W13, W2 = rand(E, 2 * I, H), rand(E, H, I)
+    return (dev_bf16(x), dev_f32(lg), w, gpu_lib.mx_quantize_expert_weights_t(W13, W2), rand(T * k, H),
+            rand(T * k, 2 * I), (T, H, E, k, I))
+
+
+def test_a_layer_on_a_stream_beside_a_busy_one(gpu_lib):
+    """Without buffers of the caller's, each result taken from buffers that are dropped at once,
+    forward and backward in turn on two streams."""
+    x, lg, w, wt, dY2, dY13, shape = layer_case(gpu_lib)
+    k = shape[3]
+    results = lambda g: [g.dhact, g.dxperm, g.dw2, g.dw13]
+
+    def step(**o):
+        out = gpu_lib.mx_moe_forward(x, lg, w, k, **o).out
+        # (the buffers are made on the stream that fills them)
+        with torch.cuda.stream(o.get("stream")):
+            f = gpu_lib.mx_alloc_forward(*shape, keep_hact=True)
+        gpu_lib.mx_moe_forward(x, lg, w, k, f, **o)
+        return [out] + results(gpu_lib.mx_moe_backward(x, f, wt, dY2, dY13, **o))
+
+    want = step()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        keep_busy()
+        got += [step(), step(stream=s), step(stream=s), step()]
+    f = gpu_lib.mx_moe_forward(x, lg, w, k, stream=s)
+    assert [pool_of(t) for t in (f.out, f.y, f.pws, f.xq.codes, f.hq.scales, f.routing.offsets)] == [s.cuda_stream] * 6
+    torch.cuda.synchronize()
+    for ts in got:
+        assert all(same_bits(a, b) for a, b in zip(ts, want))

@@ -224,3 +224,68 @@ def test_the_current_streams_call_stays_there(gpu, i, given):
     gpu.made.clear()
     call()
     assert {s for *_, s, _ in gpu.calls} == {100} == set(gpu.made.values()) and not gpu.recorded
+
+
+T, E, K_, H, I = 3, 4, 2, 64, 32
+
+
+def layer_tensors(b):
+    """Every tensor of a layer's buffers."""
+    for v in vars(b).values():
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif hasattr(v, "__dataclass_fields__"):
+            yield from layer_tensors(v)
+
+
+def forward(stream=None, bufs=None, n=T):
+    return nv4.mx_moe_forward(ten(n, H), ten(n, E, dtype=torch.float32), weights(E, H, I), K_, bufs, stream=stream)
+
+
+def backward(fwd, stream=None, bufs=None):
+    wt = nv4.MXTransposedWeights(mx(E * I, H), mx(E * H, 2 * I))
+    return nv4.mx_moe_backward(ten(T, H), fwd, wt, ten(T * K_, H), ten(T * K_, 2 * I), bufs, stream=stream)
+
+
+LAYER_CALLS = {"mxfp4_quantize", "moe_permute", "mxfp4_grouped_gemm", "moe_combine", "mx_padded_offsets"}
+
+
+@pytest.mark.parametrize("given", [None, 100, 200])
+def test_a_layer_on_a_stream_takes_the_streams_memory(gpu, given):
+    """Buffers that the layer makes (its routing among them) come from the pool of the stream that
+    writes them, so that dropping them early gives them to that stream's later work only; those it
+    returns wait for the caller's stream as well."""
+    at = given or 100
+    stream = given and Stream(given)
+    kept = nv4.mx_alloc_forward(T, H, E, K_, I, keep_hact=True)
+    gpu.made.clear()
+    f = forward(stream)
+    assert {n for n, *_ in gpu.calls} == LAYER_CALLS - {"mx_padded_offsets"} and {s for *_, s, _ in gpu.calls} == {at}
+    mine = {t.data_ptr() for t in layer_tensors(f)}
+    assert mine <= set(gpu.made) and set(gpu.made.values()) == {at}
+    assert gpu.recorded == ({a: {100} for a in mine} if at == 200 else {})
+    # buffers of the caller's stay as they are: only the routing is new
+    gpu.made.clear(), gpu.recorded.clear()
+    old = {t.data_ptr() for t in layer_tensors(kept)}
+    f = forward(stream, kept)
+    new = {t.data_ptr() for t in layer_tensors(f)} - old
+    assert len(new) == 6 and new <= set(gpu.made) and set(gpu.made.values()) == {at}
+    assert set(gpu.recorded) == (new if at == 200 else set())
+    gpu.made.clear(), gpu.recorded.clear(), gpu.calls.clear()
+    forward(stream, kept)   # routing and all: nothing is made
+    assert not gpu.made and not gpu.recorded and {s for *_, s, _ in gpu.calls} == {at}
+    gpu.calls.clear()
+    g = backward(f, stream)
+    assert {s for *_, s, _ in gpu.calls} == {at} == set(gpu.made.values())
+    assert gpu.recorded == ({t.data_ptr(): {100} for t in layer_tensors(g)} if at == 200 else {})
+    assert gpu.stream == Stream(100)
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        forward(Stream(200, "cuda:1"))
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        backward(f, Stream(200, "cuda:1"))
+
+
+def test_a_layer_refuses_host_tensors(gpu):
+    with pytest.raises(ValueError, match="GPU"):
+        nv4.mx_moe_forward(torch.zeros(T, H, dtype=BF16), torch.zeros(T, E), weights(E, H, I), K_)
+    assert not gpu.calls and not gpu.made
