@@ -352,17 +352,19 @@ def mx_quantize_expert_weights(W13: torch.Tensor, W2: torch.Tensor, rule: int = 
                                stream=None) -> MXExpertWeights:
     """W13 [E, 2I, H] and W2 [E, H, I] (BF16 or FP32) -> MXFP4 along their last dimension."""
     E, I2, H = W13.shape
-    return MXExpertWeights(mxfp4_quantize(W13.reshape(E * I2, H), rule=rule, stream=stream),
-                           mxfp4_quantize(W2.reshape(E * H, I2 // 2), rule=rule, stream=stream), E, H, I2 // 2)
+    with _Layer(stream, W13) as layer:  # (weights whose rows are not in one stride are copied here)
+        return MXExpertWeights(layer.made(mxfp4_quantize(W13.reshape(E * I2, H), rule=rule)),
+                               layer.made(mxfp4_quantize(W2.reshape(E * H, I2 // 2), rule=rule)), E, H, I2 // 2)
 
 
 def mx_quantize_expert_weights_t(W13: torch.Tensor, W2: torch.Tensor, rule: int = NV4_MX_FLOOR,
                                  stream=None) -> MXTransposedWeights:
     """W13 [E, 2I, H] and W2 [E, H, I] -> per-expert transposes in MXFP4."""
     E, I2, H = W13.shape
-    t = dict(layout=NV4_COLS_BATCHED, nseg=E, rule=rule, stream=stream)
-    return MXTransposedWeights(mxfp4_quantize(W2.reshape(E * H, I2 // 2), **t),
-                               mxfp4_quantize(W13.reshape(E * I2, H), **t))
+    t = dict(layout=NV4_COLS_BATCHED, nseg=E, rule=rule)
+    with _Layer(stream, W13) as layer:
+        return MXTransposedWeights(layer.made(mxfp4_quantize(W2.reshape(E * H, I2 // 2), **t)),
+                                   layer.made(mxfp4_quantize(W13.reshape(E * I2, H), **t)))
 
 
 @dataclass

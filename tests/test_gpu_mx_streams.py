@@ -98,3 +98,25 @@ def test_a_layer_on_a_stream_beside_a_busy_one(gpu_lib):
     torch.cuda.synchronize()
     for ts in got:
         assert all(same_bits(a, b) for a, b in zip(ts, want))
+
+
+def test_strided_weights_on_a_stream(gpu_lib):
+    """The copy of weights whose rows are not in one stride, before and behind work of its size."""
+    E, H, I = 6, 512, 256
+    g = torch.Generator("cuda").manual_seed(2)
+    W13 = torch.randn(2 * I, E, H, dtype=torch.bfloat16, device="cuda", generator=g).transpose(0, 1)
+    W2 = torch.randn(H, E, I, dtype=torch.bfloat16, device="cuda", generator=g).transpose(0, 1)
+    flat = lambda w, wt: [t for m in (w.w13, w.w2, wt.w13t, wt.w2t) for t in (m.codes, m.scales)]
+    both = lambda a, b, **o: flat(gpu_lib.mx_quantize_expert_weights(a, b, **o),
+                                  gpu_lib.mx_quantize_expert_weights_t(a, b, **o))
+    want = both(W13.contiguous(), W2.contiguous())
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        keep_busy()
+        got += [both(W13, W2, stream=s), both(W13, W2)]
+    torch.cuda.synchronize()
+    for ts in got:
+        assert all(same_bits(a, b) for a, b in zip(ts, want))
+    assert pool_of(got[0][0]) == s.cuda_stream

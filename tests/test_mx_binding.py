@@ -289,3 +289,25 @@ def test_a_layer_refuses_host_tensors(gpu):
     with pytest.raises(ValueError, match="GPU"):
         nv4.mx_moe_forward(torch.zeros(T, H, dtype=BF16), torch.zeros(T, E), weights(E, H, I), K_)
     assert not gpu.calls and not gpu.made
+
+
+@pytest.mark.parametrize("given", [None, 100, 200])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_strided_weights_are_copied_on_the_stream(gpu, given, transposed):
+    """Weights whose rows are not in one stride are copied first: on the stream that quantises them,
+    which waits for no other."""
+    stored = [ten(2 * I, E, H).transpose(0, 1), ten(H, E, I).transpose(0, 1)]
+    at = given or 100
+    quantize = nv4.mx_quantize_expert_weights_t if transposed else nv4.mx_quantize_expert_weights
+    q = quantize(*stored, stream=given and Stream(given))
+    tensors = [t for m in vars(q).values() if isinstance(m, nv4.MXFP4) for t in (m.codes, m.scales)]
+    assert [s for *_, s, _ in gpu.calls] == [at] * 2
+    copies = {a[0] for a in gpu.args("mxfp4_quantize")}
+    assert copies | {t.data_ptr() for t in tensors} == set(gpu.made) and set(gpu.made.values()) == {at}
+    assert set(gpu.recorded) == ({t.data_ptr() for t in tensors} if at == 200 else set())
+    # contiguous weights are read where they are
+    gpu.made.clear(), gpu.calls.clear()
+    held = [ten(E, 2 * I, H), ten(E, H, I)]
+    quantize(*held, stream=given and Stream(given))
+    assert {a[0] for a in gpu.args("mxfp4_quantize")} == {t.data_ptr() for t in held}
+    assert gpu.stream == Stream(100)
