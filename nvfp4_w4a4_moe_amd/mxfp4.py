@@ -299,8 +299,9 @@ def mxfp4_grouped_gemm(A: MXFP4, B: MXFP4, offsets: torch.Tensor, E: int, N: int
 # ----------------------------------------------------------------------------- layer composition
 
 class _Layer:
-    """Makes the given stream current while a layer's calls are queued on it, so that what they
-    allocate comes from its pool (as for one call, see _Call)."""
+    """Makes the given stream, or else the tensors' device, current while a layer's calls are queued
+    there: what they allocate comes from that stream's pool (as for one call, see _Call), and the
+    calls that know only the current device find it."""
 
     def __init__(self, stream, x: torch.Tensor):
         if not x.is_cuda:
@@ -308,7 +309,12 @@ class _Layer:
         if stream is not None and stream.device != x.device:
             raise ValueError(f"stream of {stream.device} for tensors on {x.device}")
         self.caller = torch.cuda.current_stream(x.device)
-        self.on = contextlib.nullcontext() if stream is None or stream == self.caller else torch.cuda.stream(stream)
+        if stream is not None and stream != self.caller:
+            self.on = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != x.get_device():
+            self.on = torch.cuda.device(x.device)
+        else:
+            self.on = contextlib.nullcontext()
 
     def __enter__(self):
         self.on.__enter__()

@@ -83,7 +83,7 @@ class Gpu:
         monkeypatch.setattr(torch.cuda, "stream", stream)
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: self.device)
-        monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: self.stream)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: self.stream if d is not None or not self.device else Stream(900))
         monkeypatch.setattr(mxfp4, "_raw_stream", lambda i: self.stream.cuda_stream)
         monkeypatch.setattr(mxfp4, "load", lambda: self)
         monkeypatch.setattr(nv4, "load", lambda: self)
@@ -311,3 +311,16 @@ def test_strided_weights_are_copied_on_the_stream(gpu, given, transposed):
     quantize(*held, stream=given and Stream(given))
     assert {a[0] for a in gpu.args("mxfp4_quantize")} == {t.data_ptr() for t in held}
     assert gpu.stream == Stream(100)
+
+
+def test_a_layer_on_another_device_than_the_current_one(gpu):
+    """Every call of the layer, moe_permute and moe_combine among them, runs with the tensors' device
+    current and on that device's stream."""
+    gpu.device = 1
+    f = forward()
+    backward(forward(None, nv4.mx_alloc_forward(T, H, E, K_, I, keep_hact=True)))
+    nv4.mx_quantize_expert_weights(ten(E, 2 * I, H), ten(E, H, I))
+    forward(Stream(200), f)
+    assert LAYER_CALLS == {n for n, *_ in gpu.calls}
+    assert {d for *_, d in gpu.calls} == {0} and {s for *_, s, _ in gpu.calls} == {100, 200}
+    assert gpu.device == 1
