@@ -346,6 +346,13 @@ class MXExpertWeights:
     I: int
 
 
+def _weight_shapes(W13: torch.Tensor, W2: torch.Tensor):
+    E, I2, H = W13.shape
+    if I2 % 2 or W2.shape != (E, H, I2 // 2):
+        raise ValueError(f"W13 [E, 2I, H] and W2 [E, H, I] must fit together, not {list(W13.shape)} and {list(W2.shape)}")
+    return E, I2, H
+
+
 @dataclass
 class MXTransposedWeights:
     """Expert weights transposed and re-quantised along their new contraction dimension (the
@@ -357,7 +364,7 @@ class MXTransposedWeights:
 def mx_quantize_expert_weights(W13: torch.Tensor, W2: torch.Tensor, rule: int = NV4_MX_FLOOR,
                                stream=None) -> MXExpertWeights:
     """W13 [E, 2I, H] and W2 [E, H, I] (BF16 or FP32) -> MXFP4 along their last dimension."""
-    E, I2, H = W13.shape
+    E, I2, H = _weight_shapes(W13, W2)
     with _Layer(stream, W13) as layer:  # (weights whose rows are not in one stride are copied here)
         return MXExpertWeights(layer.made(mxfp4_quantize(W13.reshape(E * I2, H), rule=rule)),
                                layer.made(mxfp4_quantize(W2.reshape(E * H, I2 // 2), rule=rule)), E, H, I2 // 2)
@@ -366,7 +373,7 @@ def mx_quantize_expert_weights(W13: torch.Tensor, W2: torch.Tensor, rule: int = 
 def mx_quantize_expert_weights_t(W13: torch.Tensor, W2: torch.Tensor, rule: int = NV4_MX_FLOOR,
                                  stream=None) -> MXTransposedWeights:
     """W13 [E, 2I, H] and W2 [E, H, I] -> per-expert transposes in MXFP4."""
-    E, I2, H = W13.shape
+    E, I2, H = _weight_shapes(W13, W2)
     t = dict(layout=NV4_COLS_BATCHED, nseg=E, rule=rule)
     with _Layer(stream, W13) as layer:
         return MXTransposedWeights(layer.made(mxfp4_quantize(W2.reshape(E * H, I2 // 2), **t)),
@@ -405,6 +412,15 @@ def mx_moe_forward(x: torch.Tensor, logits: torch.Tensor, w: MXExpertWeights, k:
     SwiGLU and re-quantisation in the epilogue, down product, combine (``out``)."""
     T, H = x.shape
     R = T * k
+    if H != w.H:
+        raise ValueError(f"x has {H} columns, the weights {w.H}")
+    if logits.shape != (T, w.E):
+        raise ValueError(f"logits must be [{T}, {w.E}]")
+    if bufs is not None:
+        rt = bufs.routing
+        if bufs.xq.rows != T or bufs.hq.rows != R or bufs.out.shape != x.shape or not bufs.out.is_contiguous() or \
+                rt is not None and (rt.topk_ids.shape != (T, k) or rt.offsets.numel() != w.E + 1):
+            raise ValueError(f"bufs are not those of {T} rows of {H} and {k} of {w.E} experts")
     with _Layer(stream, x) as layer:
         st = layer.stream
         if bufs is None:
@@ -464,6 +480,8 @@ def mx_moe_backward(x: torch.Tensor, fwd: MXForwardBuffers, wt: MXTransposedWeig
     T, H = x.shape
     rt = fwd.routing
     E, R, I = rt.offsets.numel() - 1, rt.row_token.numel(), fwd.hact.shape[1]
+    if rt.topk_ids.shape[0] != T:
+        raise ValueError(f"x has {T} rows, the forward's {rt.topk_ids.shape[0]}")
     with _Layer(stream, x) as layer:
         st = layer.stream
         if bufs is None:

@@ -324,3 +324,42 @@ def test_a_layer_on_another_device_than_the_current_one(gpu):
     assert LAYER_CALLS == {n for n, *_ in gpu.calls}
     assert {d for *_, d in gpu.calls} == {0} and {s for *_, s, _ in gpu.calls} == {100, 200}
     assert gpu.device == 1
+
+
+# ----------------------------------------------------------------------------- shapes
+
+def test_a_layers_inputs_fit_together(gpu):
+    """Rows, experts and buffers of another batch: the routing would be written behind its buffers,
+    or rows of x that do not exist be taken for others."""
+    f32 = torch.float32
+    fwd = lambda n=T, lg=(T, E), k=K_, h=H, bufs=None: nv4.mx_moe_forward(ten(n, h), ten(*lg, dtype=f32), weights(E, H, I),
+                                                                          k, bufs)
+    for lg in ((T + 1, E), (T - 1, E), (T, E + 1), (T * E,)):
+        with pytest.raises(ValueError, match="logits"):
+            fwd(lg=lg)
+    with pytest.raises(ValueError, match="columns"):
+        fwd(h=96)
+    alloc = lambda n=T, h=H, k=K_: nv4.mx_alloc_forward(n, h, E, k, I, keep_hact=True)
+    for other in (alloc(n=T + 1), alloc(k=1), alloc(k=3), alloc(h=96)):
+        with pytest.raises(ValueError, match="bufs"):
+            fwd(bufs=other)
+    used = fwd(bufs=alloc())
+    for field, n in (("topk_ids", (T, K_ + 1)), ("topk_ids", (T + 1, K_)), ("offsets", (E,))):
+        bad = alloc()
+        bad.routing = nv4.Routing(**{**vars(used.routing), field: ten(*n, dtype=torch.int32)})
+        with pytest.raises(ValueError, match="bufs"):
+            fwd(bufs=bad)
+    with pytest.raises(ValueError, match="bufs"):
+        strided = alloc()
+        strided.out = ten(T, H + 8)[:, :H]
+        fwd(bufs=strided)
+    gpu.calls.clear()
+    wt = nv4.MXTransposedWeights(mx(E * I, H), mx(E * H, 2 * I))
+    for n in (T - 1, T + 1, 2 * T):
+        with pytest.raises(ValueError, match="rows"):
+            nv4.mx_moe_backward(ten(n, H), used, wt, ten(T * K_, H), ten(T * K_, 2 * I))
+    for s13, s2 in (((E, 2 * I, H), (E, I, H)), ((E, 2 * I + 1, H), (E, H, I)), ((E, 2 * I, H), (E + 1, H, I))):
+        for quantize in (nv4.mx_quantize_expert_weights, nv4.mx_quantize_expert_weights_t):
+            with pytest.raises(ValueError, match="W2"):
+                quantize(ten(*s13), ten(*s2))
+    assert not gpu.calls
