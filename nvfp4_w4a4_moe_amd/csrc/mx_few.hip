@@ -477,6 +477,7 @@ __global__ __launch_bounds__(kGuThreads) void k_few_gate_up(MxFewArgs a) {
           gate += part(v, reg)[at];
           up += part(v, reg + 8)[at];
         }
+        // (mx_swiglu's steps, and its error)
         h[u] = gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
       }
       uint32_t m = max(__float_as_uint(h[0]) & 0x7FFFFFFFu, __float_as_uint(h[1]) & 0x7FFFFFFFu);

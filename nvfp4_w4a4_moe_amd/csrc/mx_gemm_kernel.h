@@ -166,7 +166,11 @@ __device__ __forceinline__ int frag_row(int i) { return ((i >> 2) & 1) * 16 + (i
 // four code dwords as the instruction's operand (FP4 reads the first four of eight)
 __device__ __forceinline__ i32x8 mx_operand(int4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
 
-// gate / (1 + exp(-gate)) * up in FP32 (hardware exp2 and reciprocal, relative error ~1e-7)
+// gate / (1 + exp(-gate)) * up in FP32, with the hardware's exp2 and reciprocal.  The exponent
+// -gate log2(e) is rounded to FP32 before exp2, so the relative error grows with the gate:
+// (1.25 |gate| + 8) 2^-24 at most, 6e-6 at -80.  A more exact exponent would take a second product
+// and an addition per value, for a result that leaves as BF16 or FP4 (half a step: 2^-8 and 2^-2).
+// Below -87.3, where the reciprocal is under FP32's smallest normal number, the result may be 0.
 __device__ __forceinline__ float mx_swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
