@@ -15,7 +15,8 @@
  *     clamped to e >= -127; A == 0 gives e = -127.
  *   scale byte = e + 127; code = E2M1_rne_sat(v / 2^e), ties to the even code;
  *   element 2i sits in the low nibble of byte i; a code is sign << 3 | magnitude index
- *   (0, .5, 1, 1.5, 2, 3, 4, 6).  The value is e2m1(code) * 2^e, which BF16 holds exactly.
+ *   (0, .5, 1, 1.5, 2, 3, 4, 6).  The value is e2m1(code) * 2^e, which BF16 holds exactly
+ *   (but for 2^128 and above, which NV4_MX_CEIL makes of 1.75 * 2^127 and more: infinity).
  *   A block with a NaN or infinity gets scale byte 255 (NaN) and codes 0, and raises
  *   NV4_DS_NONFINITE; everything computed from it is NaN.
  *   Products are exact, sums are FP32.  SwiGLU is gate / (1 + exp(-gate)) * up in FP32 with a
