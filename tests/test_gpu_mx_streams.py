@@ -120,3 +120,37 @@ def test_strided_weights_on_a_stream(gpu_lib):
     for ts in got:
         assert all(same_bits(a, b) for a, b in zip(ts, want))
     assert pool_of(got[0][0]) == s.cuda_stream
+
+
+def test_captured_on_a_forked_stream(gpu_lib):
+    """Calls with `stream` of a stream forked into a capture: their memory belongs to the graph, whose
+    replays between eager calls on either stream give the eager results."""
+    T, E, k, H, I = 20, 16, 4, 256, 64
+    x, lg, w, *_ = few_case(gpu_lib, 2 * T, E, k, H, I)
+    xs, ls = dev_bf16(x), dev_f32(lg)
+    x, lg = xs[:T].clone(), ls[:T].clone()
+    s = torch.cuda.Stream()
+
+    def step(o):
+        few = gpu_lib.mx_moe_few(x, lg, w, k, **o)
+        f = gpu_lib.mx_moe_forward(x, lg, w, k, **o)
+        return [few, f.out, gpu_lib.mxfp4_dequantize(gpu_lib.mxfp4_quantize(x, **o), **o)]
+
+    step({})
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        s.wait_stream(here)
+        got = step(dict(stream=s))
+        here.wait_stream(s)
+    for i in range(4):
+        x.copy_(xs[i * 5:i * 5 + T])
+        lg.copy_(ls[i * 5:i * 5 + T])
+        want = step({})
+        torch.cuda.synchronize()
+        beside = step(dict(stream=s))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, beside):
+            assert same_bits(a, b) and same_bits(c, b)
