@@ -32,8 +32,8 @@
 // stay: eight layers in turn, as a decode step reads them, take 42.1 us each for seven tokens
 // against 44.6; 64 tokens again and again 70 against 78, seven 39.9 against 38.2.
 //
-// Measured at H 2048, I 768, 8 of 128 experts a token, weights from memory: one token 14.9 us, seven
-// 41 (2.8 TB/s), 64 tokens 75 us (4.2 TB/s, nearly every expert's weights).
+// Measured at H 2048, I 768, 8 of 128 experts a token, even routing, weights from memory: one token
+// 14.9 us, seven 42 (2.8 TB/s), 64 tokens 74 us (4.2 TB/s, nearly every expert's weights).
 #include <algorithm>
 #include <type_traits>
 
@@ -702,8 +702,9 @@ bool few_fused(const MxFewArgs &a) { return a.logits && few_smallest(a); }
 
 // Listing the experts costs 5 us, which pay once experts have several rows each: the GEMM, and the
 // down product by experts, then read their weights once.  (Not the smallest batches: the same routing
-// has the same bits whether it is computed here or given.)  Measured in us, layers in turn, one by
-// one / grouped, by assignments:
+// has the same bits whether it is computed here or given.)  The host knows the number of assignments
+// and experts, not the routing: the rule takes it to be even.  Measured in us, layers in turn, even
+// routing, one by one / grouped, by assignments:
 //   8 experts (H 4096, I 14336)    8  106 / 113   12  143 / 130   16  163 / 141   32  240 / 151
 //   8 (H 4096, I 1536)            16 31.4 / 31.0  32 39.5 / 39.0  48 47.4 / 39.4
 //   16 (H 4096, I 4096)           16 70.2 / 77.6  24 86.3 / 88.2  32 99.7 / 88.7
@@ -712,6 +713,12 @@ bool few_fused(const MxFewArgs &a) { return a.logits && few_smallest(a); }
 //   64 (H 2048, I 1024)           48 44.4 / 51.2  72 51.4 / 52.9  96 58.8 / 55.2
 //   128 (H 2048, I 768)           72 47.2 / 51.1  96 54.2 / 54.3 112 58.7 / 55.0
 //   256 (H 2048, I 512)           64 39.2 / 42.8  96 49.0 / 55.1 128 58.1 / 59.6
+// The border moves with I as well, which the rule leaves out: at 8 experts it is below 12 assignments
+// for I 14336 and at 16 for 1536, and the rule takes 12.  On the other side of it a batch loses at
+// most 10 % (8 experts, I 14336, 12; 16 experts, 24: 88.2 for 86.3).  Every token at the same experts
+// is the rule's worst case: one by one the down product reads an expert's weights once per token
+// (64 tokens of 2 of 256 experts, I 512: 38.0 / 29.3; 64 of 1 of 128, I 768: 29.5 / 28.3), which still
+// takes less than even routing (54.0 and 42.6).
 bool few_grouped(const MxFewArgs &a) {
   return !few_smallest(a) && a.T * a.k > std::min({a.E + 4, 64 + a.E / 4, kMostRows});
 }

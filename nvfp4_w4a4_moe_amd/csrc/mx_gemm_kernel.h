@@ -27,11 +27,17 @@
 // and every epilogue the same number of branch-free stores, so a wait counts exactly what may
 // still be under way.
 //
-// Measured: 8192 x 8192 x 8192 3.4-3.8 PFLOP/s; gate and up of 131072 skewed rows of 128 experts (K
-// 2048, N 768) 295 us, 2.8 PFLOP/s, bound by the matrix cores, with a tenth of the time for the
-// SwiGLU and its stores; 768 rows of 128 experts 43 us, 5.0 TB/s of weights.  With K = 768 a tile is
-// three stages, and its stores bound it: loads return in order behind them, so the third
-// stage waits for them (FP32 weight gradients of 64 experts, 403 MB: 105 us, 70 without stores).
+// Measured: 8192 x 8192 x 8192 3.3-3.5 PFLOP/s; 768 rows of 128 experts 43 us, 5.0 TB/s of weights.
+// Gate and up of 131072 skewed rows of 128 experts (K 2048, N 768) 290 to 330 us with BF16 rows (by
+// inputs and clock), 272 with the re-quantised result alone, 300 with both, 454 with it and FP32
+// rows.  No unit is full there: by counters the matrix cores are busy for 34 % of the cycles (2.8 of
+// the 8.1 PFLOP/s above), 0.69 GB are moved at 2.4 TB/s, and a wave waits for 40 % of its cycles,
+// for the next stage's loads and at the barriers, with one other wave on its SIMD.
+// With K = 768 a tile is three stages, and its stores bound it: loads return in order behind them, so
+// the third stage waits for them (FP32 weight gradients of 64 experts, 403 MB: 105 us, 70 without
+// stores).  More and shorter stages in the same LDS (four of K = 128 instead of two of 256, large
+// tile) were slower throughout: weight gradients 115, BF16 rows of K = 768 60 for 55, gate and up
+// 358 for 320, 8192 x 8192 x 8192 396 for 318.
 #pragma once
 
 #include <algorithm>
@@ -80,10 +86,13 @@ struct MxTile {
   static constexpr int kWaveCodeRows = kCodeDma * kCodeRows, kWaveScaleRows = kScaleDma * kScaleRows;
   static_assert(kWaveCodeRows <= 64 && kWaveScaleRows <= 64, "a lane for each row");
   static constexpr bool kSameRows = kWaveCodeRows == kWaveScaleRows;
-  // The smallest tile is for a few rows per expert: no other tile reads its part of B, which is then
-  // streamed past the caches and leaves them to A.  Eight layers' weights in turn (128 experts,
-  // 1536 x 2048, 768 rows): 49.2 -> 44.1 us; one layer's, which the 256 MB cache would hold,
-  // again and again: 37.6 -> 43.6.
+  // The smallest tile is for a few rows per expert in the mean: then hardly another tile reads its
+  // part of B, which is streamed past the caches and leaves them to A.  Cached -> streamed, eight
+  // layers' weights in turn (128 experts, 1536 x 2048): 768 rows 49.2 -> 44.1 us, 4096 rows 48.7 ->
+  // 44.4.  With uneven loads several tiles of an expert stream the same weights, and the gain
+  // goes: one expert with two thirds of 768 rows 53.1 -> 50.8, with half of 4096 56.2 -> 54.7, 4096 rows
+  // by Zipf's law (1.1) 55.8 -> 55.6.  One layer's weights again and again, which the 256 MB
+  // cache would hold, lose by it: 37.5 -> 42.4, uneven 42.8 to 45.0 -> 49.8 to 54.4.
   static constexpr bool kStreamB = BM == 64;
   // every wave loads rows of one operand only
   static constexpr bool kOneSide = kSameRows && BN % kWaveCodeRows == 0 && BM % kWaveCodeRows == 0;

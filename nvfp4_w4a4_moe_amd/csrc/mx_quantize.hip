@@ -12,10 +12,15 @@
 // a 32-row block of one dword column (two BF16 columns or one FP32).
 //
 // Measured, 131072 x 2048 BF16 (537 MB in, 143 MB out per direction): rows 114 us (6.0 TB/s), columns
-// 140 (4.8), both from one read 175 (4.7), columns of rows gathered from 16384 tokens 92 (120 behind
-// other work), values back 94 (7.2).  The column form is bound by its pieces: 256 bytes of a
-// row in, 64 bytes of a column and its scale bytes out (tiles of 256 rows x 128 bytes, whole lines
-// out, were no faster).
+// 140 (4.9), both from one read 178 (4.6), values back 95 (7.1).  The column form is bound by its
+// pieces: 256 bytes of a row in, 64 bytes of a column and its scale bytes out (tiles of 256 rows x
+// 128 bytes, whole lines out, were no faster).
+// Columns of rows gathered from 16384 tokens: 104 us for the same tokens again, 113 to 122 for others
+// each time; 65536 rows from 8192 tokens 51.  By counters about 240 MB are fetched and 150 written
+// (65536 rows: 43 and 80, the columns of x that are in use staying in L2): 3.3 (2.4) TB/s, so
+// memory does not bound it.  A wave waits for 60 % of its cycles: a tile is one chain of dependent
+// loads (padded total, segment, row index, row), which four workgroups per CU (33 KB of LDS each)
+// do not hide.
 #include <algorithm>
 
 #include "mx_device.h"

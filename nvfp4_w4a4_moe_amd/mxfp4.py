@@ -11,6 +11,10 @@ power-of-two scale, the 4-bit format gfx950's matrix instructions multiply as it
 ``mx_moe_forward`` and ``mx_moe_backward`` compose them with moe_permute and moe_combine as
 ``moe_forward`` and ``moe_backward`` do for NVFP4.  Everything here is reachable from the
 package's top level.
+
+Matrices may have any row stride of at least their width.  With ``stream`` a call, or a whole
+layer, runs on that stream, and what it allocates comes from that stream's pool; the stream waits
+for no other, so inputs have to be ready there and results be waited for by whoever reads them.
 """
 
 from __future__ import annotations
