@@ -352,7 +352,7 @@ class MXExpertWeights:
 
 def _weight_shapes(W13: torch.Tensor, W2: torch.Tensor):
     E, I2, H = W13.shape
-    if I2 % 2 or W2.shape != (E, H, I2 // 2):
+    if I2 % 2 or W2.shape not in ((E, H, I2 // 2), (E * H, I2 // 2)):
         raise ValueError(f"W13 [E, 2I, H] and W2 [E, H, I] must fit together, not {list(W13.shape)} and {list(W2.shape)}")
     return E, I2, H
 

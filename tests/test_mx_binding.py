@@ -363,3 +363,11 @@ def test_a_layers_inputs_fit_together(gpu):
             with pytest.raises(ValueError, match="W2"):
                 quantize(ten(*s13), ten(*s2))
     assert not gpu.calls
+
+
+def test_weights_given_as_matrices(gpu):
+    """W2 as [E*H, I], which its rows are in memory anyway."""
+    for quantize in (nv4.mx_quantize_expert_weights, nv4.mx_quantize_expert_weights_t):
+        gpu.calls.clear()
+        quantize(ten(E, 2 * I, H), ten(E * H, I))
+        assert sorted(a[3:5] for a in gpu.args("mxfp4_quantize")) == sorted([(E * 2 * I, H), (E * H, I)])
