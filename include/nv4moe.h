@@ -469,6 +469,8 @@ nv4_status moe_combine(const void *Y, nv4_dtype ytype, int64_t ldy, const int32_
 }
 #endif
 
-#include "nv4moe/mxfp4.h" /* the MXFP4 calls */
+#include "nv4moe/mxfp4.h"  /* the MXFP4 calls */
+#include "nv4moe/fp8.h"    /* the FP8 calls */
+#include "nv4moe/router.h" /* the router's losses and gradients */
 
 #endif /* NV4MOE_H */

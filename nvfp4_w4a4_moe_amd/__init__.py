@@ -19,7 +19,10 @@ its four backward grouped GEMMs.  ``moe_forward_bf16`` is the unquantised layer
 and ``moe_backward_bf16`` the backward on BF16 operands: the forward's NVFP4
 tensors dequantised (the dequantized backward) or the BF16 tensors themselves.
 The MXFP4 calls (mxfp4_quantize, mxfp4_dequantize, mxfp4_grouped_gemm, the layer
-mx_moe_forward / mx_moe_backward and its decode form mx_moe_few) are in mxfp4.py and
+mx_moe_forward / mx_moe_backward and its decode form mx_moe_few) are in mxfp4.py, the
+FP8 calls (fp8_quantize, fp8_dequantize, fp8_transpose, fp8_grouped_gemm, the layer
+fp8_moe_forward / fp8_moe_backward) in fp8.py and the router's losses and gradients
+(moe_balance_loss, moe_balance_backward, moe_combine_backward) in router.py, all
 reachable from here.
 There is no fallback: if the library is not built, every call raises.
 """
@@ -926,3 +929,5 @@ def nv4_bench_lds(out: torch.Tensor | None, iters: int, stream=None) -> tuple:
 # ----------------------------------------------------------------------------- MXFP4
 
 from .mxfp4 import *  # noqa: E402,F401,F403  (needs the names above)
+from .fp8 import *  # noqa: E402,F401,F403
+from .router import *  # noqa: E402,F401,F403

@@ -22,7 +22,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
-from dataclasses import dataclass
+from dataclasses import dataclass, is_dataclass
 
 import torch
 
@@ -335,7 +335,7 @@ class _Layer:
             for v in vars(bufs).values():
                 if isinstance(v, torch.Tensor):
                     v.record_stream(self.caller)
-                elif isinstance(v, MXFP4):
+                elif is_dataclass(v):  # a quantised tensor
                     self.made(v)
         return bufs
 

@@ -35,6 +35,8 @@ moe       routing, permutation, grouped GEMMs, SwiGLU and the weighted combine.
 pipeline  the whole expert-layer forward and backward with the GPU's storage
           roundings mirrored (for end-to-end reporting).
 mxfp4     MXFP4 block quantisation (32 elements, power-of-two scales) and its layer.
+fp8       FP8 (E4M3) quantisation with an FP32 scale for each block of 128.
+router    the balance and z losses with their gradients, and the combine's gradients.
 philox    the Philox4x64-10 counter-based generator (stochastic rounding).
 
 Parity status: every function is pinned by tests under ``tests/`` against
@@ -49,4 +51,4 @@ FP4 rounding boundary, so the GPU tests compare stage by stage, each stage fed t
 GPU's own inputs, and gate the whole layer only loosely.
 """
 
-from . import formats, philox, nvfp4, moe, mxfp4, pipeline  # noqa: F401
+from . import formats, philox, nvfp4, moe, mxfp4, fp8, router, pipeline  # noqa: F401
