@@ -16,6 +16,17 @@
 //     |products|: a hundredth of BF16's rounding, and less beside that of the codes.
 //   FP32 results: v_mfma_f32_32x32x16_f16 on the codes converted to FP16, which holds E4M3 exactly: exact
 //     products and FP32 sums, at half the rate.
+//
+// Power-of-two scales on both operands go into the scaled instruction (v_mfma_scale_f32_32x32x64_f8f6f4 takes an
+// exponent byte for each row), which then adds onto the accumulators itself.
+//
+// Pipeline.  Codes and scales come to LDS by DMA, in stages of one block, into a ring of kStages slots.  The
+// stages of all of a workgroup's tiles are one sequence: the loads run kStages ahead of the products, across
+// tile ends and under the epilogue.  A wave takes a stage's token fragments into registers and then
+// one weight fragment after the other, the next one's LDS reads under way.  Before the last weight
+// fragment's products every wave waits for its own loads of the next stage, the workgroup meets, and the
+// slot just read is refilled.  Every stage issues the same number of loads (a load with nothing to fetch has
+// an offset behind the buffer), so a wait counts exactly what may still be under way.
 #pragma once
 
 #include <algorithm>
@@ -30,32 +41,87 @@
 namespace nv4 {
 namespace {
 
-// WAVES_M x WAVES_N waves of FM x FN 32 x 32 fragments, stages of one block (K = 128)
-template <int WAVES_M, int WAVES_N, int FM, int FN>
+// WAVES_M x WAVES_N waves of FM x FN 32 x 32 fragments; a ring of STAGES stages of one block (K = 128)
+template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES, int WAVES_PER_SIMD>
 struct F8Tile {
   static constexpr int kWavesM = WAVES_M, kWavesN = WAVES_N, kFM = FM, kFN = FN;
+  static constexpr int kStages = STAGES, kWavesPerSimd = WAVES_PER_SIMD;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int BM = WAVES_M * FM * 32;  // rows of A (tokens)
   static constexpr int BN = WAVES_N * FN * 32;  // rows of B (weights)
   static constexpr int BK = 128;
   static constexpr int kRows = BM + BN;
-  static constexpr int kCodeDma = kRows / 8 / NW;  // 1 KB each: 8 rows of 128 bytes
-  static constexpr int kScaleDma = (kRows / 64 + NW - 1) / NW;
-  static constexpr int kStageBytes = kRows * 128;
-  static_assert(kRows % (8 * NW) == 0 && BN % 64 == 0 && BM % 64 == 0, "DMA blocks of one operand");
+  static constexpr int kCodeDma = kRows / 8 / NW;                // per wave, 1 KB each: 8 rows of 128 bytes
+  static constexpr int kScaleDma = (kRows + 64 * NW - 1) / (64 * NW);  // per wave, 64 rows of 4 bytes each
+  static constexpr int kDma = kCodeDma + kScaleDma;              // the same for every wave
+  static constexpr int kScaleBase = kRows * 128;
+  static constexpr int kStageBytes = kScaleBase + NW * kScaleDma * 256;
+  // tile rows whose codes, and whose scales, one wave loads, and how many of them a lane looks up
+  static constexpr int kWaveRows = kCodeDma * 8, kWaveScaleRows = kScaleDma * 64;
+  static constexpr int kLook = (kWaveRows + 63) / 64;
+  static constexpr bool kSameRows = kWaveRows == kWaveScaleRows;
+  static_assert(kRows % (8 * NW) == 0 && BN % 64 == 0, "DMAs of one operand");
+  // every wave loads rows of one operand only
+  static constexpr bool kOneSide = BN % kWaveRows == 0 && (kSameRows || BN % kWaveScaleRows == 0);
+  // with one wave on a SIMD, a pair's scaling runs under its own next products
+  static constexpr bool kAhead = WAVES_PER_SIMD == 1;
+  // The smallest tile is for a few rows per expert in the mean: hardly another tile reads its part of B, which
+  // is streamed past the caches.
+  static constexpr bool kStreamB = BM <= 64;
 };
+
+// LDS DMA as mx_dma16 and mx_dma4, in assembly: a builtin's load into the ring makes the compiler wait for every load
+// in flight before the next LDS read that it cannot tell apart from it, which is most of them (the waits and
+// barriers here are placed by hand).  lds: the wave's LDS byte address.  No register is written but m0, which
+// nothing else in these kernels uses.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return i32x4{(int)p, (int)(p >> 32) & 0xFFFF, (int)bytes, 0x00020000};
+}
+template <bool STREAM>
+__device__ __forceinline__ void f8_dma16(i32x4 buffer, uint32_t lds, uint32_t voff) {
+  if (STREAM)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(voff),
+                 "s"(buffer)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
+                 "s"(buffer)
+                 : "memory");
+}
+__device__ __forceinline__ void f8_dma4(i32x4 buffer, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buffer)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t f8_lds(const void *p) {
+  return __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)static_cast<const uint8_t *>(p));
+}
+
+template <class T>
+__device__ __forceinline__ const __attribute__((address_space(3))) T *f8_lds_ptr(uint32_t at) {
+  return (const __attribute__((address_space(3))) T *)(uintptr_t)at;
+}
 
 // ring position of 16-byte chunk q of tile row r: the rows of one LDS read pass cover all banks
 __device__ __forceinline__ int f8_swz(int q, int r) { return q ^ ((r >> 1) & 7); }
 
-// A lane's 64 codes of one row and block, as the instruction's operands.  (The order of K is the same for both
+// a lane's 64 codes of one row and block
+struct F8Raw {
+  i32x4 c[4];
+};
+// They as the instruction's operands.  (The order of K is the same for both
 // operands, whatever it is.)
 template <bool WIDE>
 struct F8Frag {
   i32x8 v[2];
-  __device__ __forceinline__ void set(int4 a, int4 b, int4 c, int4 d) {
-    v[0] = i32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    v[1] = i32x8{c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+  __device__ __forceinline__ void set(const F8Raw &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const i32x4 a = r.c[2 * i], b = r.c[2 * i + 1];
+      v[i] = i32x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
   }
 };
 __device__ __forceinline__ f16x8 f8_to_f16(int lo, int hi) {
@@ -65,11 +131,15 @@ __device__ __forceinline__ f16x8 f8_to_f16(int lo, int hi) {
 template <>
 struct F8Frag<true> {
   f16x8 v[8];
-  __device__ __forceinline__ void set(int4 a, int4 b, int4 c, int4 d) {
-    v[0] = f8_to_f16(a.x, a.y), v[1] = f8_to_f16(a.z, a.w), v[2] = f8_to_f16(b.x, b.y), v[3] = f8_to_f16(b.z, b.w);
-    v[4] = f8_to_f16(c.x, c.y), v[5] = f8_to_f16(c.z, c.w), v[6] = f8_to_f16(d.x, d.y), v[7] = f8_to_f16(d.z, d.w);
+  __device__ __forceinline__ void set(const F8Raw &r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = f8_to_f16(r.c[i].x, r.c[i].y);
+      v[2 * i + 1] = f8_to_f16(r.c[i].z, r.c[i].w);
+    }
   }
 };
+typedef uint32_t f8_u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ f32x16 f8_product(const F8Frag<false> &w, const F8Frag<false> &t) {
   f32x16 p = {};
   p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w.v[0], t.v[0], p, 0, 0, 0, 0, 0, 0);
@@ -82,18 +152,46 @@ __device__ __forceinline__ f32x16 f8_product(const F8Frag<true> &w, const F8Frag
   return p;
 }
 
-template <class Cfg, int GROUP, int EPI, bool OUT_F32, bool QUANT>
-__global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
-  constexpr int BM = Cfg::BM, BN = Cfg::BN, FM = Cfg::kFM, FN = Cfg::kFN, NT = Cfg::NT;
-  constexpr bool SWIGLU = EPI == NV4_EPI_SWIGLU;
-  constexpr bool K_GROUPS = GROUP == NV4_GROUP_K;
+// Transposes 16-byte pieces in groups of G lanes: piece k of lane i becomes piece i of lane k.
+template <int G>
+__device__ __forceinline__ void f8_exchange(f8_u32x4 (&c)[G], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < G; bit *= 2) {
+    const bool odd = lane & bit;
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      if (k & bit) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t x = c[k][r], y = c[k + bit][r];
+        // the neighbour's: lane ^ 1 (quad_perm [1,0,3,2]) or lane ^ 2 ([2,3,0,1])
+        const uint32_t nx = (uint32_t)(bit == 1 ? __builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false)
+                                                : __builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false));
+        const uint32_t ny = (uint32_t)(bit == 1 ? __builtin_amdgcn_mov_dpp((int)y, 0xB1, 0xF, 0xF, false)
+                                                : __builtin_amdgcn_mov_dpp((int)y, 0x4E, 0xF, 0xF, false));
+        c[k][r] = odd ? ny : x;
+        c[k + bit][r] = odd ? y : nx;
+      }
+    }
+  }
+}
+
+template <class Cfg, int GROUP, int EPI, bool OUT_F32, bool QUANT, bool POW2>
+__global__ __launch_bounds__(Cfg::NT) __attribute__((amdgpu_waves_per_eu(Cfg::kWavesPerSimd)))
+void k_f8_gemm(F8GemmArgs g) {
+  constexpr int BM = Cfg::BM, BN = Cfg::BN, FM = Cfg::kFM, FN = Cfg::kFN, NT = Cfg::NT, S = Cfg::kStages;
+  constexpr bool SWIGLU = EPI == NV4_EPI_SWIGLU, K_GROUPS = GROUP == NV4_GROUP_K;
   constexpr int NF = SWIGLU ? FN / 2 : FN;  // 32-column fragments of the result
   constexpr int ESZ = OUT_F32 ? 4 : 2;
   static_assert(!QUANT || (SWIGLU && BN == 256), "a quantised block is the tile's 128 result columns");
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[Cfg::kStageBytes];
-  __shared__ __attribute__((aligned(256))) float ring_s[Cfg::NW * Cfg::kScaleDma * 64];
+  static_assert(!SWIGLU || FN % 2 == 0, "a wave's gate fragments and their up fragments");
+  static_assert(!POW2 || !OUT_F32, "FP32 results take the converted codes");
+  static_assert(S == 2 || S == 3, "a tile's row indices land within one stage of the loads");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * Cfg::kStageBytes];
   __shared__ int tab[kMxMaxExperts + 1];
   __shared__ int off[kMxMaxExperts + 1];
+  __shared__ int rows_c[Cfg::NW][Cfg::kLook * 64], rows_s[Cfg::kSameRows ? 1 : Cfg::NW][Cfg::kWaveScaleRows];
+  __shared__ int4 jobs[Cfg::NW][4];
   __shared__ uint32_t s_max[QUANT ? Cfg::kWavesN : 1][QUANT ? BM : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -101,10 +199,10 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
   const int h = lane >> 5, l32 = lane & 31;
   const int64_t kb = (g.K + 127) / 128;
   const uint32_t ld = (uint32_t)g.K, sld = (uint32_t)kb * 4;
+  const uint32_t a_bytes = (uint32_t)(g.a_rows * g.K), a_sbytes = (uint32_t)(g.a_rows * sld);
   // B is addressed from the tile's expert, so that only one expert's part must stay below 4 GiB
   const int64_t b_rows = K_GROUPS ? g.b_rows : (SWIGLU ? 2 : 1) * g.N;
   const int64_t b_srows = K_GROUPS ? g.b_rows : (b_rows + 127) / 128;
-  const uint32_t a_bytes = (uint32_t)(g.a_rows * g.K), a_sbytes = (uint32_t)(g.a_rows * sld);
   const uint32_t b_bytes = (uint32_t)(b_rows * g.K), b_sbytes = (uint32_t)(b_srows * sld);
 
   // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty)
@@ -112,102 +210,183 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
   __syncthreads();
   MxTiles<Cfg, GROUP, EPI, F8GemmArgs> tiles{g, off, tab, 0, 0, 0, 0, 0, 0};
   tiles_setup(g, off, tab, reinterpret_cast<int *>(ring), tiles);
-
-#pragma unroll 1
-  for (int it = 0; tiles.has(it); ++it) {
-    MxJob j = tiles.get(it);
-    if (K_GROUPS && j.k_len > 0) {  // whole blocks
-      const int hi = j.k_lo + j.k_len;
-      j.k_lo &= ~127;
-      j.nst = (hi - j.k_lo + 127) / 128;
-    }
-    const int64_t first = K_GROUPS ? 0 : (int64_t)j.e * b_rows;
-    const uint8_t *b_codes = g.b_codes + first * g.K;
-    const float *b_scales = g.b_scales + (K_GROUPS ? 0 : (int64_t)j.e * b_srows * kb);
-    const auto a_row = [&](int r) MX_INLINE -> int {  // A row of tile row r (behind the weights), or -1
-      int row = j.m0 + r - BN;
-      if (row >= j.m_end) return -1;
-      if (!K_GROUPS && g.a_rows_index) row = min(max(g.a_rows_index[row], 0), (int)g.a_rows - 1);
-      return row;
+  // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included)
+  uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
+  const int qrow = lane >> 3, qpos = lane & 7;  // row and ring position in a code DMA
+  MxJob pj{};     // the loading tile (the loads are up to kStages tiles ahead of the products, and leave them here)
+  int4(&queue)[4] = jobs[wave];
+  int p_it = -1;  // its number in this workgroup's sequence
+  int p_st = 0;   // its next stage
+  bool p_live = true;  // there is one
+  bool primed = false;
+  const bool gather = !K_GROUPS && g.a_rows_index != nullptr;
+  // Row indices of a tile come through LDS as well: each wave loads its lanes' own (a row of B
+  // or none has the offset behind the buffer) well before they are needed.
+  const auto load_index = [&](const MxJob &j) MX_INLINE {
+    const auto one = [&](int r, int *dst) MX_INLINE {
+      const int row = j.m0 + (r - BN);
+      f8_dma4(f8_buffer(g.a_rows_index, (uint32_t)g.M_cap * 4u), f8_lds(dst),
+              r >= BN && r < BN + BM && row < j.m_end ? (uint32_t)row * 4u : kNoRow);
     };
-    uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
+#pragma unroll
+    for (int l = 0; l < Cfg::kLook; ++l) one(wave * Cfg::kWaveRows + l * 64 + lane, rows_c[wave] + l * 64);
+    if constexpr (!Cfg::kSameRows) {
+#pragma unroll
+      for (int l = 0; l < Cfg::kScaleDma; ++l) one(wave * Cfg::kWaveScaleRows + l * 64 + lane, rows_s[wave] + l * 64);
+    }
+  };
+  // operand row of tile row r, or -1; idx: what load_index brought
+  const auto p_row = [&](int r, const int *idx) MX_INLINE -> int {
+    int row = pj.m0 + (r - BN);
+    row = r < BN + BM && row < pj.m_end ? row : -1;
+    if (gather && row >= 0) row = min(max(mx_table(idx + lane), 0), (int)g.a_rows - 1);
+    if (r < BN) row = mx_b_row<Cfg, GROUP, EPI, true>(g, pj, r);
+    return row;
+  };
+  const uint8_t *b_codes = g.b_codes;  // the expert's
+  const float *b_scales = g.b_scales;
+  const auto p_setup = [&]() MX_INLINE {
+    if (!K_GROUPS) {
+      b_codes = g.b_codes + (int64_t)pj.e * b_rows * g.K;
+      b_scales = g.b_scales + (int64_t)pj.e * b_srows * kb;
+    }
+    int mc[Cfg::kLook], ms[Cfg::kScaleDma];
+#pragma unroll
+    for (int l = 0; l < Cfg::kLook; ++l) mc[l] = p_row(wave * Cfg::kWaveRows + l * 64 + lane, rows_c[wave] + l * 64);
+#pragma unroll
+    for (int l = 0; l < Cfg::kScaleDma; ++l)
+      ms[l] = Cfg::kSameRows ? mc[l] : p_row(wave * Cfg::kWaveScaleRows + l * 64 + lane, rows_s[wave] + l * 64);
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
-      const int r = (wave * Cfg::kCodeDma + i) * 8 + (lane >> 3);
-      const int row = r < BN ? mx_b_row<Cfg, GROUP, EPI, true>(g, j, r) : a_row(r);
-      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(f8_swz(lane & 7, r) * 16);
+      const int in = i * 8 + qrow, row = __shfl(mc[i / 8], in & 63, 64);
+      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(f8_swz(qpos, wave * Cfg::kWaveRows + in) * 16);
     }
 #pragma unroll
-    for (int i = 0; i < Cfg::kScaleDma; ++i) {
-      const int r = (wave * Cfg::kScaleDma + i) * 64 + lane;
-      int row = r < BN ? mx_b_row<Cfg, GROUP, EPI, true>(g, j, r) : r < BN + BM ? a_row(r) : -1;
-      if (!K_GROUPS && r < BN && row >= 0) row >>= 7;
-      off_s[i] = row < 0 ? kNoRow : (uint32_t)row * sld;
+    for (int l = 0; l < Cfg::kScaleDma; ++l) {
+      const bool of_b = wave * Cfg::kWaveScaleRows + l * 64 + lane < BN;
+      off_s[l] = ms[l] < 0 ? kNoRow : (uint32_t)(!K_GROUPS && of_b ? ms[l] >> 7 : ms[l]) * sld;
     }
-    f32x16 acc[FN][FM];
+  };
+  // The loads go on to the next tile, as long as there is one with a stage (GROUP_K's empty ones come last).  Its
+  // row indices were fetched when the tile before was begun, at least one stage's wait ago; before the first
+  // stage (primed) they are waited for.
+  const auto next_tile = [&]() MX_INLINE {
+    p_live = tiles.has(++p_it);
+    if (p_live) {
+      pj = tiles.get(p_it);
+      if (K_GROUPS && pj.k_len > 0) {  // whole blocks
+        const int hi = pj.k_lo + pj.k_len;
+        pj.k_lo &= ~127;
+        pj.nst = (hi - pj.k_lo + 127) / 128;
+      }
+      p_live = pj.nst > 0;
+      if (p_live && lane == 0) queue[p_it & 3] = make_int4(pj.e | pj.nt << 10, pj.m0, pj.m_end, pj.nst);
+    }
+    p_st = 0;
+    if (!p_live) return;
+    if (gather && !primed) {
+      if (p_it == 0) load_index(pj);
+      mx_wait_vm<0>();
+    }
+    p_setup();
+    if (gather && tiles.has(p_it + 1)) {
+      mx_wait_lds();  // (this tile's indices have been read)
+      load_index(tiles.get(p_it + 1));
+    }
+  };
+  // the sequence's next stage into the slot at LDS address dst
+  const auto load_stage = [&](uint32_t dst) MX_INLINE {
+    if (p_live && (p_it < 0 || p_st == pj.nst)) next_tile();
+    const uint32_t k0 = (uint32_t)(pj.k_lo + p_st * 128);
+    const int left = p_live ? (int)g.K - (int)k0 : 0;  // elements behind k0 (may exceed the block)
+    const auto code_buffer = [&](bool of_b) MX_INLINE {
+      return f8_buffer(of_b ? b_codes : g.a_codes, of_b ? b_bytes : a_bytes);
+    };
+    const bool mine = wave * Cfg::kWaveRows < BN;
+    const i32x4 own = code_buffer(mine);
+#pragma unroll
+    for (int i = 0; i < Cfg::kCodeDma; ++i) {
+      const int b = wave * Cfg::kCodeDma + i;
+      const bool in_k = f8_swz(qpos, b * 8 + qrow) * 16 < left;
+      // (saturating: without a row the sum stays behind the buffer)
+      const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], k0) : kNoRow;
+      const bool of_b = Cfg::kOneSide ? mine : b * 8 < BN;
+      const i32x4 buffer = Cfg::kOneSide ? own : code_buffer(of_b);
+      if (Cfg::kStreamB && of_b) f8_dma16<true>(buffer, dst + b * 1024, v);
+      else f8_dma16<false>(buffer, dst + b * 1024, v);
+    }
+#pragma unroll
+    for (int l = 0; l < Cfg::kScaleDma; ++l) {
+      const int b = wave * Cfg::kScaleDma + l;
+      const uint32_t v = left > 0 ? __builtin_elementwise_add_sat(off_s[l], k0 / 128 * 4) : kNoRow;
+      const bool of_b = b * 64 < BN;
+      f8_dma4(f8_buffer(of_b ? b_scales : g.a_scales, of_b ? b_sbytes : a_sbytes), dst + Cfg::kScaleBase + b * 256, v);
+    }
+    ++p_st;
+  };
+  const uint32_t ring_at = f8_lds(ring);
+#pragma unroll
+  for (int s = 0; s < S; ++s) load_stage(ring_at + s * Cfg::kStageBytes);
+  primed = true;
+  mx_wait_vm<(S - 1) * Cfg::kDma>();
+  mx_barrier();
+
+  // ---- fragments of one stage: lane half h takes chunks 4 h .. 4 h + 3 of a row
+  constexpr bool MANY = K_GROUPS && !POW2;  // a scale for each weight row
+  F8Raw tr[FM], wr;
+  F8Frag<OUT_F32> tf[FM], wf;
+  float sa[FM], sb[MANY ? 16 : 1], nb[MANY ? 16 : 1];
+  const int w_row = wn * FN * 32, t_row = BN + wm * FM * 32;
+  // LDS addresses are integers: slots, fragments and rows differ by multiples of 128, the chunks of a row by the low
+  // bits that the swizzle permutes
+  const uint32_t lane_at = (uint32_t)(l32 * 128 + f8_swz(h * 4, l32) * 16);
+  const auto raw = [&](uint32_t st, int row0) MX_INLINE {
+    const uint32_t at = lane_at + (st + row0 * 128);
+    F8Raw r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r.c[q] = *f8_lds_ptr<i32x4>(at ^ (q * 16));
+    return r;
+  };
+  const auto read_tokens = [&](uint32_t st, int f) MX_INLINE { tr[f] = raw(st, t_row + f * 32); };
+  const auto read_scales = [&](uint32_t st) MX_INLINE {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa[f] = *f8_lds_ptr<float>(st + Cfg::kScaleBase + (t_row + f * 32 + l32) * 4);
+  };
+  // weight fragment i and its scales (into nb)
+  const auto read_weights = [&](uint32_t st, int i) MX_INLINE {
+    const int row0 = w_row + i * 32;
+    wr = raw(st, row0);
+    const uint32_t at = st + Cfg::kScaleBase + row0 * 4;
+    if constexpr (POW2) {
+      nb[0] = *f8_lds_ptr<float>(at + l32 * 4);
+    } else if constexpr (K_GROUPS) {
+      // register r: operand row 8 (r / 4) + 4 h + r % 4
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 t = *f8_lds_ptr<f32x4>(at + 8 * q * 4 + 4 * h * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) nb[4 * q + r] = t[r];
+      }
+    } else {
+      nb[0] = *f8_lds_ptr<float>(at);  // a fragment's 32 rows lie in one block of 128
+    }
+  };
+
+  f32x16 acc[FN][FM];
+  const auto clear = [&]() MX_INLINE {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int f = 0; f < FM; ++f)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][f][r] = 0.0f;
-    for (int st = 0; st < j.nst; ++st) {
-      const uint32_t k0 = (uint32_t)(j.k_lo + st * 128);
-      __syncthreads();  // the last stage has been read
-#pragma unroll
-      for (int i = 0; i < Cfg::kCodeDma; ++i) {
-        const int b = wave * Cfg::kCodeDma + i;
-        const bool in_k = k0 + f8_swz(lane & 7, b * 8 + (lane >> 3)) * 16 < (uint32_t)g.K;
-        const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], k0) : kNoRow;
-        if (b * 8 < BN) mx_dma16(b_codes, b_bytes, ring + b * 1024, v);
-        else mx_dma16(g.a_codes, a_bytes, ring + b * 1024, v);
-      }
-#pragma unroll
-      for (int i = 0; i < Cfg::kScaleDma; ++i) {
-        const int b = wave * Cfg::kScaleDma + i;
-        const uint32_t v = __builtin_elementwise_add_sat(off_s[i], k0 / 128 * 4);
-        if (b * 64 < BN) mx_dma4(b_scales, b_sbytes, reinterpret_cast<uint8_t *>(ring_s + b * 64), v);
-        else mx_dma4(g.a_scales, a_sbytes, reinterpret_cast<uint8_t *>(ring_s + b * 64), v);
-      }
-      mx_wait_vm<0>();
-      __syncthreads();
-      const auto operand = [&](int row) MX_INLINE {
-        const auto chunk = [&](int q) MX_INLINE {
-          return *reinterpret_cast<const int4 *>(ring + row * 128 + f8_swz(h * 4 + q, row) * 16);
-        };
-        F8Frag<OUT_F32> f;
-        f.set(chunk(0), chunk(1), chunk(2), chunk(3));
-        return f;
-      };
-      F8Frag<OUT_F32> tf[FM];
-      float sa[FM];
-#pragma unroll
-      for (int f = 0; f < FM; ++f) {
-        const int row = BN + (wm * FM + f) * 32 + l32;
-        tf[f] = operand(row);
-        sa[f] = ring_s[row];
-      }
-#pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const int row0 = (wn * FN + i) * 32;
-        const F8Frag<OUT_F32> w = operand(row0 + l32);
-#pragma unroll
-        for (int f = 0; f < FM; ++f) {
-          const f32x16 p = f8_product(w, tf[f]);
-          const float s = sa[f] * ring_s[row0];
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            // register r: weight row 8 (r / 4) + 4 h + r % 4 of the operand, column 16 h + r of the result
-            const float sr = K_GROUPS ? sa[f] * ring_s[row0 + 8 * (r / 4) + 4 * h + r % 4] : s;
-            acc[i][f][r] = __builtin_fmaf(p[r], sr, acc[i][f][r]);
-          }
-        }
-      }
-    }
+  };
 
-    // ---- epilogue: lane = row l32 of a fragment, registers = columns 16 h + r
+  // ---- a finished tile: lane = row l32 of a fragment, registers = columns 16 h + r.  (A 16-byte store may start at
+  // any dword.)
+  const auto finish = [&](const MxJob &j) MX_INLINE {
     const int ncols = (int)(K_GROUPS ? g.b_rows : g.N);
-    const int col_w = j.nt * (SWIGLU ? BN / 2 : BN) + wn * NF * 32;
+    const int col_w = j.nt * (SWIGLU ? BN / 2 : BN) + wn * NF * 32;  // this wave's first column
     const int64_t row_w = (int64_t)j.m0 + wm * FM * 32;
     const int rows = (int)std::min<int64_t>(std::max<int64_t>(j.m_end - row_w, 0), FM * 32);
     if constexpr (SWIGLU) {
@@ -219,20 +398,47 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
           for (int r = 0; r < 16; ++r) acc[i][f][r] = mx_swiglu(acc[i][f][r], acc[i + NF][f][r]);
     }
     if (!QUANT || g.C) {
+      const int ldc = (int)g.ldc;
       char *cb = static_cast<char *>(g.C) + ((K_GROUPS ? (int64_t)j.e * g.a_rows : 0) + row_w) * g.ldc * ESZ;
+      // rows behind the valid ones fall behind the buffer
+      const auto dst = __builtin_amdgcn_make_buffer_rsrc(mx_uniform_ptr(cb), (short)0, rows * ldc * ESZ, 0x00020000);
+      // A lane's 16-byte pieces of its row, G at a time (one FP32 fragment's, two BF16 fragments'), change places in its
+      // group of G lanes: each store then writes whole lines, G pieces side by side.
+      constexpr int PER = 16 / ESZ, G = OUT_F32 || NF > 1 ? 4 : 2, FRAGS = G / ESZ;
+      const int gl = lane & (G - 1);
+      const int col_g = col_w + (gl / ESZ) * 32 + h * 16 + (gl % ESZ) * PER;  // this lane's piece of a group's first fragment
+      const bool dwords = OUT_F32 || ((int64_t)reinterpret_cast<uintptr_t>(g.C) | g.ldc * ESZ) % 4 == 0;
+      const bool ragged = !dwords || (ncols % PER != 0 && col_w + NF * 32 > ncols);
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
-        const int rw = f * 32 + l32;
-        if (rw >= rows) continue;
 #pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          const int col = col_w + i * 32 + h * 16;
-          char *p = cb + ((int64_t)rw * g.ldc + col) * ESZ;
+        for (int i = 0; i < NF; i += FRAGS) {
+          f8_u32x4 c[G];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            if (col + r >= ncols) continue;
-            if constexpr (OUT_F32) reinterpret_cast<float *>(p)[r] = acc[i][f][r];
-            else reinterpret_cast<__bf16 *>(p)[r] = (__bf16)acc[i][f][r];
+          for (int q = 0; q < G; ++q) {
+            const f32x16 &x = acc[i + q / ESZ][f];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if constexpr (OUT_F32) c[q][r] = __float_as_uint(x[4 * q + r]);
+              else
+                c[q][r] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x[8 * (q % 2) + 2 * r], (__bf16)x[8 * (q % 2) + 2 * r + 1]});
+            }
+          }
+          f8_exchange<G>(c, lane);
+          const int col = col_g + i * 32;
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            const uint32_t at = (uint32_t)((f * 32 + (l32 & ~(G - 1)) + k) * ldc + col) * ESZ;
+            const bool piece = dwords && col + PER <= ncols;
+            __builtin_amdgcn_raw_buffer_store_b128(c[k], dst, piece ? at : kNoStore, 0, kStream);
+            if (ragged) {  // one by one: the piece over the last column, and rows that start between dwords
+#pragma unroll
+              for (int r = 0; r < PER; ++r) {
+                const uint32_t v = !piece && col + r < ncols ? at + r * ESZ : kNoStore;
+                if constexpr (OUT_F32) __builtin_amdgcn_raw_buffer_store_b32(c[k][r], dst, v, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(c[k][r / 2] >> (16 * (r & 1))), dst, v, 0, 0);
+              }
+            }
           }
         }
       }
@@ -250,7 +456,8 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
         const auto sm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
         if (h == 0) s_max[wn][(wm * FM + f) * 32 + l32] = max(sm[0], sm[1]);
       }
-      __syncthreads();
+      mx_wait_lds();
+      mx_barrier();
       const int64_t qkb = (ncols + 127) / 128;
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
@@ -266,7 +473,8 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
             uint32_t c[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              c[q] = s.bad ? 0u : f8_pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3], s.S);
+              c[q] = s.bad ? 0u
+                           : f8_pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3], s.S);
             if (col < ncols)
               *reinterpret_cast<uint4 *>(g.q_codes + (row_w + rw) * ncols + col) = make_uint4(c[0], c[1], c[2], c[3]);
           }
@@ -274,11 +482,127 @@ __global__ __launch_bounds__(Cfg::NT) void k_f8_gemm(F8GemmArgs g) {
         }
       }
     }
+  };
+
+  // ---- products
+  // A fragment pair's sum over the block goes onto the accumulators under the block's scales: while the
+  // SIMD's other wave multiplies, or (kAhead) under the next pair's products, from one of two buffers.
+  constexpr int NP = Cfg::kAhead && !POW2 ? 2 : 1;
+  f32x16 p[NP];
+  float ps = 0.0f, pb[MANY && NP == 2 ? 16 : 1];  // the waiting sum's scales
+  const auto multiply = [&](int i, int f) MX_INLINE {
+    if constexpr (POW2) {
+      // the exponent bytes of both rows' scales (a NaN's is 255, which is NaN there too)
+      const int ws = (int)(__float_as_uint(sb[0]) >> 23), ts = (int)(__float_as_uint(sa[f]) >> 23);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        acc[i][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf.v[s], tf[f].v[s], acc[i][f], 0, 0, 0, ws, 0, ts);
+      asm volatile("" : "+v"(acc[i][f]));
+    } else {
+      p[(i * FM + f) % NP] = f8_product(wf, tf[f]);
+      // (products stay where they are written: they touch no memory, so nothing else keeps the compiler
+      // from moving them past the reads, for which the registers do not last)
+      if constexpr (NP == 2) asm volatile("" : "+v"(p[(i * FM + f) % NP]));
+    }
+  };
+  const auto collect = [&](int i, int f) MX_INLINE {
+    if constexpr (!POW2) {
+      const float s = NP == 2 ? ps : MANY ? sa[f] : sa[f] * sb[0];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float sr = !MANY ? s : s * (NP == 2 ? pb[NP == 2 ? r : 0] : sb[r]);
+        acc[i][f][r] = __builtin_fmaf(p[(i * FM + f) % NP][r], sr, acc[i][f][r]);
+      }
+      asm volatile("" : "+v"(acc[i][f]));
+    }
+  };
+  const auto products = [&](int i, int f) MX_INLINE {
+    multiply(i, f);
+    if constexpr (NP == 2) {
+      // the pair before, in the stage before's last fragment if this is the first
+      const int n = (i * FM + f + FN * FM - 1) % (FN * FM);
+      collect(n / FM, n % FM);
+      ps = MANY ? sa[f] : sa[f] * sb[0];
+      if constexpr (MANY) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) pb[r] = sb[r];
+      }
+    } else {
+      collect(i, f);
+    }
+  };
+  int slot = 0, next_slot = Cfg::kStageBytes;
+  // the stage has been read by this wave: wait for its own loads of the next one, meet, and refill
+  const auto turn = [&]() MX_INLINE {
+    mx_wait_lds();
+    mx_wait_vm<(S - 2) * Cfg::kDma>();
+    mx_barrier();
+    load_stage(ring_at + slot);
+    slot = next_slot;
+    next_slot = next_slot == (S - 1) * Cfg::kStageBytes ? 0 : next_slot + Cfg::kStageBytes;
+  };
+#pragma unroll 1
+  for (int it = 0; tiles.has(it); ++it) {
+    MxJob cj;
+    if (p_live || it < p_it) {
+      const int *q = reinterpret_cast<const int *>(&queue[it & 3]);
+      const int x = __builtin_amdgcn_readfirstlane(q[0]);
+      cj.e = x & 1023;
+      cj.nt = x >> 10;
+      cj.m0 = __builtin_amdgcn_readfirstlane(q[1]);
+      cj.m_end = __builtin_amdgcn_readfirstlane(q[2]);
+      cj.nst = __builtin_amdgcn_readfirstlane(q[3]);
+    } else {  // behind the last tile that has been loaded
+      cj = tiles.get(it);
+      cj.nst = 0;
+    }
+    clear();
+    // (the waves behind an expert's last row leave the matrix cores to the others)
+    if (K_GROUPS || cj.m0 + wm * FM * 32 < cj.m_end) {
+      if (cj.nst > 0) {
+        read_weights(ring_at + slot, 0);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) read_tokens(ring_at + slot, f);
+        read_scales(ring_at + slot);
+      }
+      if constexpr (NP == 2) {  // nothing waits yet
+        ps = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) p[1][r] = 0.0f;
+#pragma unroll
+        for (int r = 0; r < (MANY ? 16 : 1); ++r) pb[r] = 0.0f;
+      }
+#pragma unroll 1
+      for (int st = 0; st < cj.nst; ++st) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          wf.set(wr);
+#pragma unroll
+          for (int r = 0; r < (MANY ? 16 : 1); ++r) sb[r] = nb[r];
+          if (i == FN - 1) turn();
+          read_weights(ring_at + slot, i < FN - 1 ? i + 1 : 0);
+#pragma unroll
+          for (int f = 0; f < FM; ++f) {
+            if (i == 0) tf[f].set(tr[f]);
+            products(i, f);
+            if (i == FN - 1) read_tokens(ring_at + slot, f);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        read_scales(ring_at + slot);
+      }
+      if constexpr (NP == 2) collect(FN - 1, FM - 1);
+    } else {
+#pragma unroll 1
+      for (int st = 0; st < cj.nst; ++st) turn();
+    }
+    finish(cj);
   }
+  mx_wait_vm<0>();  // loads into this workgroup's LDS end before it does
 }
 
 // persistent grid: whole multiples of the XCDs
-template <class Cfg, int GROUP, int EPI>
+template <class Cfg, int GROUP, int EPI, bool OUT_F32, bool QUANT = false>
 hipError_t f8_launch(const F8GemmArgs &g, hipStream_t stream) {
   constexpr int cols = EPI == NV4_EPI_SWIGLU ? Cfg::BN / 2 : Cfg::BN;
   int64_t tiles;
@@ -289,17 +613,18 @@ hipError_t f8_launch(const F8GemmArgs &g, hipStream_t stream) {
     tiles = (int64_t)g.E * ((g.a_rows + Cfg::BM - 1) / Cfg::BM) * ((g.b_rows + Cfg::BN - 1) / Cfg::BN);
     if (tiles == 0) return hipSuccess;
   }
-  const int64_t most = (int64_t)device_cu_count() * 2;
+  const int lds = Cfg::kStages * Cfg::kStageBytes + (kMxMaxExperts + 1) * 8 +
+                  Cfg::NW * ((Cfg::kLook * 64 + Cfg::kWaveScaleRows) * 4 + 64) + (QUANT ? Cfg::kWavesN * Cfg::BM * 4 : 0);
+  const int per_cu = std::max(1, std::min(160 * 1024 / lds, Cfg::kWavesPerSimd * 4 / Cfg::NW));
+  const int64_t most = (int64_t)device_cu_count() * per_cu;
   const unsigned grid = (unsigned)std::min<int64_t>((tiles + kMxXcds - 1) / kMxXcds * kMxXcds, most);
-  if constexpr (EPI == NV4_EPI_SWIGLU && Cfg::BN == 256) {
-    if (g.q_codes) {
-      if (g.c_is_f32) k_f8_gemm<Cfg, GROUP, EPI, true, true><<<grid, Cfg::NT, 0, stream>>>(g);
-      else k_f8_gemm<Cfg, GROUP, EPI, false, true><<<grid, Cfg::NT, 0, stream>>>(g);
+  if constexpr (!OUT_F32) {
+    if (g.pow2) {
+      k_f8_gemm<Cfg, GROUP, EPI, OUT_F32, QUANT, true><<<grid, Cfg::NT, 0, stream>>>(g);
       return hipGetLastError();
     }
   }
-  if (g.c_is_f32) k_f8_gemm<Cfg, GROUP, EPI, true, false><<<grid, Cfg::NT, 0, stream>>>(g);
-  else k_f8_gemm<Cfg, GROUP, EPI, false, false><<<grid, Cfg::NT, 0, stream>>>(g);
+  k_f8_gemm<Cfg, GROUP, EPI, OUT_F32, QUANT, false><<<grid, Cfg::NT, 0, stream>>>(g);
   return hipGetLastError();
 }
 
