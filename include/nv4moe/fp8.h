@@ -124,6 +124,8 @@ nv4_status fp8_transpose(const nv4_f8_tensor *q, nv4_f8_tensor *out, void *strea
  *   mx_padded_offsets; others are taken to the blocks that they touch); C [E][N][ldc] gets
  *   A_e . B_e^T, zeros for an empty range.
  *   offsets   device int32 [E+1], 1 <= E <= 1024
+ * A call's result depends on its arguments alone, bit for bit; a call with other outputs or another
+ *   M_cap may add a row's blocks in another order.
  * A, and an expert's part of B (GROUP_K: B), each stay below 4 GiB of codes; C has at most 2^20
  * columns, ldc included.
  * No workspace.  Errors: EINVAL (shapes, an operand's nseg), EALIGN (K % 16, SwiGLU with N % 32,

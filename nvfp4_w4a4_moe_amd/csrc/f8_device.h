@@ -36,6 +36,13 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t amax_bits, int pow2) {
   return r;
 }
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+// eight codes as FP16, exactly
+__device__ __forceinline__ f16x8 f8_to_f16(int lo, int hi) {
+  const f16x2 a = e4m3x2_to_f16(lo), b = e4m3x2_to_f16<true>(lo), c = e4m3x2_to_f16(hi), d = e4m3x2_to_f16<true>(hi);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 // four values times S as E4M3 codes (gfx950's converter rounds to nearest even)
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d, float S) {
   const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(a * S, b * S, 0, false);

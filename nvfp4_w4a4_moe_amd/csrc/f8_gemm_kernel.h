@@ -56,15 +56,9 @@ struct F8Tile {
   static constexpr int kDma = kCodeDma + kScaleDma;              // the same for every wave
   static constexpr int kScaleBase = kRows * 128;
   static constexpr int kStageBytes = kScaleBase + NW * kScaleDma * 256;
-  // tile rows whose codes, and whose scales, one wave loads, and how many of them a lane looks up
-  static constexpr int kWaveRows = kCodeDma * 8, kWaveScaleRows = kScaleDma * 64;
-  static constexpr int kLook = (kWaveRows + 63) / 64;
-  static constexpr bool kSameRows = kWaveRows == kWaveScaleRows;
-  static_assert(kRows % (8 * NW) == 0 && BN % 64 == 0, "DMAs of one operand");
-  // every wave loads rows of one operand only
-  static constexpr bool kOneSide = BN % kWaveRows == 0 && (kSameRows || BN % kWaveScaleRows == 0);
-  // with one wave on a SIMD, a pair's scaling runs under its own next products
-  static constexpr bool kAhead = WAVES_PER_SIMD == 1;
+  static constexpr int kDmaB = BN / 8 / NW;  // the first of a wave's code DMAs, which fetch weights
+  static constexpr int kLook = (kCodeDma * 8 + 63) / 64;  // rows of its code DMAs that a lane looks up
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BN % 64 == 0, "DMAs of one operand");
   // The smallest tile is for a few rows per expert in the mean: hardly another tile reads its part of B, which
   // is streamed past the caches.
   static constexpr bool kStreamB = BM <= 64;
@@ -74,7 +68,6 @@ struct F8Tile {
 // in flight before the next LDS read that it cannot tell apart from it, which is most of them (the waits and
 // barriers here are placed by hand).  lds: the wave's LDS byte address.  No register is written but m0, which
 // nothing else in these kernels uses.
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   return i32x4{(int)p, (int)(p >> 32) & 0xFFFF, (int)bytes, 0x00020000};
@@ -104,6 +97,8 @@ __device__ __forceinline__ const __attribute__((address_space(3))) T *f8_lds_ptr
   return (const __attribute__((address_space(3))) T *)(uintptr_t)at;
 }
 
+constexpr int kQueue = 8;  // tiles between the loads and the products, and the one being multiplied
+
 // ring position of 16-byte chunk q of tile row r: the rows of one LDS read pass cover all banks
 __device__ __forceinline__ int f8_swz(int q, int r) { return q ^ ((r >> 1) & 7); }
 
@@ -124,10 +119,6 @@ struct F8Frag {
     }
   }
 };
-__device__ __forceinline__ f16x8 f8_to_f16(int lo, int hi) {
-  const f16x2 a = e4m3x2_to_f16(lo), b = e4m3x2_to_f16<true>(lo), c = e4m3x2_to_f16(hi), d = e4m3x2_to_f16<true>(hi);
-  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 template <>
 struct F8Frag<true> {
   f16x8 v[8];
@@ -186,12 +177,12 @@ void k_f8_gemm(F8GemmArgs g) {
   static_assert(!QUANT || (SWIGLU && BN == 256), "a quantised block is the tile's 128 result columns");
   static_assert(!SWIGLU || FN % 2 == 0, "a wave's gate fragments and their up fragments");
   static_assert(!POW2 || !OUT_F32, "FP32 results take the converted codes");
-  static_assert(S == 2 || S == 3, "a tile's row indices land within one stage of the loads");
+  static_assert(S >= 2 && S < kQueue && (S - 1) * Cfg::kDma < 64, "ring of a few slots");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[S * Cfg::kStageBytes];
   __shared__ int tab[kMxMaxExperts + 1];
   __shared__ int off[kMxMaxExperts + 1];
-  __shared__ int rows_c[Cfg::NW][Cfg::kLook * 64], rows_s[Cfg::kSameRows ? 1 : Cfg::NW][Cfg::kWaveScaleRows];
-  __shared__ int4 jobs[Cfg::NW][4];
+  __shared__ int rows_c[Cfg::NW][Cfg::kLook * 64], rows_s[Cfg::NW][Cfg::kScaleDma * 64];
+  __shared__ int4 jobs[Cfg::NW][kQueue];
   __shared__ uint32_t s_max[QUANT ? Cfg::kWavesN : 1][QUANT ? BM : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -214,12 +205,16 @@ void k_f8_gemm(F8GemmArgs g) {
   uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
   const int qrow = lane >> 3, qpos = lane & 7;  // row and ring position in a code DMA
   MxJob pj{};     // the loading tile (the loads are up to kStages tiles ahead of the products, and leave them here)
-  int4(&queue)[4] = jobs[wave];
+  int4(&queue)[kQueue] = jobs[wave];
   int p_it = -1;  // its number in this workgroup's sequence
   int p_st = 0;   // its next stage
   bool p_live = true;  // there is one
   bool primed = false;
   const bool gather = !K_GROUPS && g.a_rows_index != nullptr;
+  // Block b of eight tile rows is wave b % NW's code DMA b / NW; 64 rows' scales are one DMA.  The rows that this lane
+  // looks up, 64 at a time (the last ones may lie behind the tile):
+  const auto code_row = [&](int l) MX_INLINE { return ((l * 8 + qrow) * Cfg::NW + wave) * 8 + qpos; };
+  const auto scale_row = [&](int l) MX_INLINE { return (wave * Cfg::kScaleDma + l) * 64 + lane; };
   // Row indices of a tile come through LDS as well: each wave loads its lanes' own (a row of B
   // or none has the offset behind the buffer) well before they are needed.
   const auto load_index = [&](const MxJob &j) MX_INLINE {
@@ -229,11 +224,9 @@ void k_f8_gemm(F8GemmArgs g) {
               r >= BN && r < BN + BM && row < j.m_end ? (uint32_t)row * 4u : kNoRow);
     };
 #pragma unroll
-    for (int l = 0; l < Cfg::kLook; ++l) one(wave * Cfg::kWaveRows + l * 64 + lane, rows_c[wave] + l * 64);
-    if constexpr (!Cfg::kSameRows) {
+    for (int l = 0; l < Cfg::kLook; ++l) one(code_row(l), rows_c[wave] + l * 64);
 #pragma unroll
-      for (int l = 0; l < Cfg::kScaleDma; ++l) one(wave * Cfg::kWaveScaleRows + l * 64 + lane, rows_s[wave] + l * 64);
-    }
+    for (int l = 0; l < Cfg::kScaleDma; ++l) one(scale_row(l), rows_s[wave] + l * 64);
   };
   // operand row of tile row r, or -1; idx: what load_index brought
   const auto p_row = [&](int r, const int *idx) MX_INLINE -> int {
@@ -252,25 +245,25 @@ void k_f8_gemm(F8GemmArgs g) {
     }
     int mc[Cfg::kLook], ms[Cfg::kScaleDma];
 #pragma unroll
-    for (int l = 0; l < Cfg::kLook; ++l) mc[l] = p_row(wave * Cfg::kWaveRows + l * 64 + lane, rows_c[wave] + l * 64);
+    for (int l = 0; l < Cfg::kLook; ++l) mc[l] = p_row(code_row(l), rows_c[wave] + l * 64);
 #pragma unroll
-    for (int l = 0; l < Cfg::kScaleDma; ++l)
-      ms[l] = Cfg::kSameRows ? mc[l] : p_row(wave * Cfg::kWaveScaleRows + l * 64 + lane, rows_s[wave] + l * 64);
+    for (int l = 0; l < Cfg::kScaleDma; ++l) ms[l] = p_row(scale_row(l), rows_s[wave] + l * 64);
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
-      const int in = i * 8 + qrow, row = __shfl(mc[i / 8], in & 63, 64);
-      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(f8_swz(qpos, wave * Cfg::kWaveRows + in) * 16);
+      const int row = __shfl(mc[i / 8], (i * 8 + qrow) & 63, 64);
+      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(f8_swz(qpos, (i * Cfg::NW + wave) * 8 + qrow) * 16);
     }
 #pragma unroll
     for (int l = 0; l < Cfg::kScaleDma; ++l) {
-      const bool of_b = wave * Cfg::kWaveScaleRows + l * 64 + lane < BN;
+      const bool of_b = scale_row(l) < BN;
       off_s[l] = ms[l] < 0 ? kNoRow : (uint32_t)(!K_GROUPS && of_b ? ms[l] >> 7 : ms[l]) * sld;
     }
   };
   // The loads go on to the next tile, as long as there is one with a stage (GROUP_K's empty ones come last).  Its
-  // row indices were fetched when the tile before was begun, at least one stage's wait ago; before the first
-  // stage (primed) they are waited for.
+  // row indices were fetched when the tile before was begun: S - 2 stages' loads later they have landed with what
+  // every stage waits for; before the first stage (primed) and behind a shorter tile they are waited for.
   const auto next_tile = [&]() MX_INLINE {
+    const int before = pj.nst;
     p_live = tiles.has(++p_it);
     if (p_live) {
       pj = tiles.get(p_it);
@@ -280,11 +273,11 @@ void k_f8_gemm(F8GemmArgs g) {
         pj.nst = (hi - pj.k_lo + 127) / 128;
       }
       p_live = pj.nst > 0;
-      if (p_live && lane == 0) queue[p_it & 3] = make_int4(pj.e | pj.nt << 10, pj.m0, pj.m_end, pj.nst);
+      if (p_live && lane == 0) queue[p_it % kQueue] = make_int4(pj.e | pj.nt << 10, pj.m0, pj.m_end, pj.nst);
     }
     p_st = 0;
     if (!p_live) return;
-    if (gather && !primed) {
+    if (gather && (!primed || before < S - 2)) {
       if (p_it == 0) load_index(pj);
       mx_wait_vm<0>();
     }
@@ -294,36 +287,38 @@ void k_f8_gemm(F8GemmArgs g) {
       load_index(tiles.get(p_it + 1));
     }
   };
-  // the sequence's next stage into the slot at LDS address dst
-  const auto load_stage = [&](uint32_t dst) MX_INLINE {
-    if (p_live && (p_it < 0 || p_st == pj.nst)) next_tile();
-    const uint32_t k0 = (uint32_t)(pj.k_lo + p_st * 128);
-    const int left = p_live ? (int)g.K - (int)k0 : 0;  // elements behind k0 (may exceed the block)
-    const auto code_buffer = [&](bool of_b) MX_INLINE {
-      return f8_buffer(of_b ? b_codes : g.a_codes, of_b ? b_bytes : a_bytes);
-    };
-    const bool mine = wave * Cfg::kWaveRows < BN;
-    const i32x4 own = code_buffer(mine);
+  // the sequence's next stage into the slot at LDS address dst, in PARTS parts
+  uint32_t l_k0 = 0;
+  int l_left = 0;
+  const auto load_part = [&](uint32_t dst, int part, int parts) MX_INLINE {
+    if (part == 0) {
+      if (p_live && (p_it < 0 || p_st == pj.nst)) next_tile();
+      l_k0 = (uint32_t)(pj.k_lo + p_st * 128);
+      l_left = p_live ? (int)g.K - (int)l_k0 : 0;  // elements behind k0 (may exceed the block)
+      ++p_st;
+    }
+    const i32x4 buffer_a = f8_buffer(g.a_codes, a_bytes), buffer_b = f8_buffer(b_codes, b_bytes);
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
-      const int b = wave * Cfg::kCodeDma + i;
-      const bool in_k = f8_swz(qpos, b * 8 + qrow) * 16 < left;
+      if (i * parts / Cfg::kCodeDma != part) continue;
+      const int b = i * Cfg::NW + wave;
+      const bool in_k = f8_swz(qpos, b * 8 + qrow) * 16 < l_left;
       // (saturating: without a row the sum stays behind the buffer)
-      const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], k0) : kNoRow;
-      const bool of_b = Cfg::kOneSide ? mine : b * 8 < BN;
-      const i32x4 buffer = Cfg::kOneSide ? own : code_buffer(of_b);
-      if (Cfg::kStreamB && of_b) f8_dma16<true>(buffer, dst + b * 1024, v);
-      else f8_dma16<false>(buffer, dst + b * 1024, v);
+      const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], l_k0) : kNoRow;
+      if (i >= Cfg::kDmaB) f8_dma16<false>(buffer_a, dst + b * 1024, v);
+      else f8_dma16<Cfg::kStreamB>(buffer_b, dst + b * 1024, v);
     }
+    if (part == parts - 1) {
 #pragma unroll
-    for (int l = 0; l < Cfg::kScaleDma; ++l) {
-      const int b = wave * Cfg::kScaleDma + l;
-      const uint32_t v = left > 0 ? __builtin_elementwise_add_sat(off_s[l], k0 / 128 * 4) : kNoRow;
-      const bool of_b = b * 64 < BN;
-      f8_dma4(f8_buffer(of_b ? b_scales : g.a_scales, of_b ? b_sbytes : a_sbytes), dst + Cfg::kScaleBase + b * 256, v);
+      for (int l = 0; l < Cfg::kScaleDma; ++l) {
+        const int b = wave * Cfg::kScaleDma + l;
+        const uint32_t v = l_left > 0 ? __builtin_elementwise_add_sat(off_s[l], l_k0 / 128 * 4) : kNoRow;
+        const bool of_b = b * 64 < BN;
+        f8_dma4(f8_buffer(of_b ? b_scales : g.a_scales, of_b ? b_sbytes : a_sbytes), dst + Cfg::kScaleBase + b * 256, v);
+      }
     }
-    ++p_st;
   };
+  const auto load_stage = [&](uint32_t dst) MX_INLINE { load_part(dst, 0, 1); };
   const uint32_t ring_at = f8_lds(ring);
 #pragma unroll
   for (int s = 0; s < S; ++s) load_stage(ring_at + s * Cfg::kStageBytes);
@@ -486,34 +481,38 @@ void k_f8_gemm(F8GemmArgs g) {
 
   // ---- products
   // A fragment pair's sum over the block goes onto the accumulators under the block's scales: while the
-  // SIMD's other wave multiplies, or (kAhead) under the next pair's products, from one of two buffers.
-  constexpr int NP = Cfg::kAhead && !POW2 ? 2 : 1;
+  // SIMD's other wave multiplies, or, where the registers last for it, from one of two buffers under its own next
+  // pair's products as well (8192^3 with FP32 results 997 -> 940 us).
+  constexpr int NP = OUT_F32 && !MANY && FM * FN <= 4 ? 2 : 1;
   f32x16 p[NP];
-  float ps = 0.0f, pb[MANY && NP == 2 ? 16 : 1];  // the waiting sum's scales
+  float ps = 0.0f;  // the waiting sum's scale
   const auto multiply = [&](int i, int f) MX_INLINE {
-    if constexpr (POW2) {
-      // the exponent bytes of both rows' scales (a NaN's is 255, which is NaN there too)
-      const int ws = (int)(__float_as_uint(sb[0]) >> 23), ts = (int)(__float_as_uint(sa[f]) >> 23);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        acc[i][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf.v[s], tf[f].v[s], acc[i][f], 0, 0, 0, ws, 0, ts);
-      asm volatile("" : "+v"(acc[i][f]));
-    } else {
-      p[(i * FM + f) % NP] = f8_product(wf, tf[f]);
-      // (products stay where they are written: they touch no memory, so nothing else keeps the compiler
-      // from moving them past the reads, for which the registers do not last)
-      if constexpr (NP == 2) asm volatile("" : "+v"(p[(i * FM + f) % NP]));
-    }
+    p[(i * FM + f) % NP] = f8_product(wf, tf[f]);
+    // (products stay where they are written: they touch no memory, so nothing else keeps the compiler
+    // from moving them past the reads, for which the registers do not last)
+    if constexpr (NP == 2) asm volatile("" : "+v"(p[(i * FM + f) % NP]));
   };
   const auto collect = [&](int i, int f) MX_INLINE {
-    if constexpr (!POW2) {
-      const float s = NP == 2 ? ps : MANY ? sa[f] : sa[f] * sb[0];
+    const float s = NP == 2 ? ps : MANY ? sa[f] : sa[f] * sb[0];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float sr = !MANY ? s : s * (NP == 2 ? pb[NP == 2 ? r : 0] : sb[r]);
-        acc[i][f][r] = __builtin_fmaf(p[(i * FM + f) % NP][r], sr, acc[i][f][r]);
-      }
-      asm volatile("" : "+v"(acc[i][f]));
+    for (int r = 0; r < 16; ++r) {
+      acc[i][f][r] = __builtin_fmaf(p[(i * FM + f) % NP][r], MANY ? s * sb[MANY ? r : 0] : s, acc[i][f][r]);
+    }
+    asm volatile("" : "+v"(acc[i][f]));
+  };
+  // Power-of-two scales: straight onto the accumulators, a fragment's tokens in turn (no product waits for the one
+  // before).  The scales are the exponent bytes of both rows' (a NaN's is 255, which is NaN there too).
+  const auto scaled_products = [&](int i) MX_INLINE {
+    if constexpr (POW2) {
+      const int ws = (int)(__float_as_uint(sb[0]) >> 23);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+          acc[i][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf.v[s], tf[f].v[s], acc[i][f], 0, 0, 0, ws, 0,
+                                                                       (int)(__float_as_uint(sa[f]) >> 23));
+#pragma unroll
+      for (int f = 0; f < FM; ++f) asm volatile("" : "+v"(acc[i][f]));
     }
   };
   const auto products = [&](int i, int f) MX_INLINE {
@@ -522,22 +521,23 @@ void k_f8_gemm(F8GemmArgs g) {
       // the pair before, in the stage before's last fragment if this is the first
       const int n = (i * FM + f + FN * FM - 1) % (FN * FM);
       collect(n / FM, n % FM);
-      ps = MANY ? sa[f] : sa[f] * sb[0];
-      if constexpr (MANY) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) pb[r] = sb[r];
-      }
+      ps = sa[f] * sb[0];
     } else {
       collect(i, f);
     }
   };
+  // A slot is refilled in parts, behind the products of its last weight fragment and, where a wave has four, of
+  // the next stage's first: DMAs issued at once keep the wave from its products (gate and up of 131072 rows
+  // 486 us, in two parts 472, in four 459; in six 472).
+  constexpr int SPREAD = FN >= 4 ? 1 : 0, PARTS = (1 + SPREAD) * FM;
   int slot = 0, next_slot = Cfg::kStageBytes;
   // the stage has been read by this wave: wait for its own loads of the next one, meet, and refill
-  const auto turn = [&]() MX_INLINE {
+  const auto meet = [&]() MX_INLINE {
     mx_wait_lds();
     mx_wait_vm<(S - 2) * Cfg::kDma>();
     mx_barrier();
-    load_stage(ring_at + slot);
+  };
+  const auto turn = [&]() MX_INLINE {
     slot = next_slot;
     next_slot = next_slot == (S - 1) * Cfg::kStageBytes ? 0 : next_slot + Cfg::kStageBytes;
   };
@@ -545,7 +545,7 @@ void k_f8_gemm(F8GemmArgs g) {
   for (int it = 0; tiles.has(it); ++it) {
     MxJob cj;
     if (p_live || it < p_it) {
-      const int *q = reinterpret_cast<const int *>(&queue[it & 3]);
+      const int *q = reinterpret_cast<const int *>(&queue[it % kQueue]);
       const int x = __builtin_amdgcn_readfirstlane(q[0]);
       cj.e = x & 1023;
       cj.nt = x >> 10;
@@ -569,9 +569,8 @@ void k_f8_gemm(F8GemmArgs g) {
         ps = 0.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) p[1][r] = 0.0f;
-#pragma unroll
-        for (int r = 0; r < (MANY ? 16 : 1); ++r) pb[r] = 0.0f;
       }
+      uint32_t done = 0;  // the slot being refilled
 #pragma unroll 1
       for (int st = 0; st < cj.nst; ++st) {
 #pragma unroll
@@ -579,22 +578,46 @@ void k_f8_gemm(F8GemmArgs g) {
           wf.set(wr);
 #pragma unroll
           for (int r = 0; r < (MANY ? 16 : 1); ++r) sb[r] = nb[r];
-          if (i == FN - 1) turn();
+          if (i == FN - 1) {
+            meet();
+            done = ring_at + slot;
+            turn();
+          }
           read_weights(ring_at + slot, i < FN - 1 ? i + 1 : 0);
+          if (POW2) {
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+              if (i == 0) tf[f].set(tr[f]);
+            scaled_products(i);
+          }
 #pragma unroll
           for (int f = 0; f < FM; ++f) {
-            if (i == 0) tf[f].set(tr[f]);
-            products(i, f);
-            if (i == FN - 1) read_tokens(ring_at + slot, f);
+            if (!POW2) {
+              if (i == 0) tf[f].set(tr[f]);
+              products(i, f);
+            }
+            if (i < SPREAD && st > 0) load_part(done, (i + 1) * FM + f, PARTS);
+            if (i == FN - 1) {
+              load_part(done, f, PARTS);
+              read_tokens(ring_at + slot, f);
+            }
             __builtin_amdgcn_sched_barrier(0);
           }
         }
         read_scales(ring_at + slot);
       }
+      if (cj.nst > 0) {
+#pragma unroll
+        for (int n = FM; n < PARTS; ++n) load_part(done, n, PARTS);
+      }
       if constexpr (NP == 2) collect(FN - 1, FM - 1);
     } else {
 #pragma unroll 1
-      for (int st = 0; st < cj.nst; ++st) turn();
+      for (int st = 0; st < cj.nst; ++st) {
+        meet();
+        load_stage(ring_at + slot);
+        turn();
+      }
     }
     finish(cj);
   }
@@ -614,7 +637,7 @@ hipError_t f8_launch(const F8GemmArgs &g, hipStream_t stream) {
     if (tiles == 0) return hipSuccess;
   }
   const int lds = Cfg::kStages * Cfg::kStageBytes + (kMxMaxExperts + 1) * 8 +
-                  Cfg::NW * ((Cfg::kLook * 64 + Cfg::kWaveScaleRows) * 4 + 64) + (QUANT ? Cfg::kWavesN * Cfg::BM * 4 : 0);
+                  Cfg::NW * ((Cfg::kLook * 64 + Cfg::kScaleDma * 64) * 4 + kQueue * 16) + (QUANT ? Cfg::kWavesN * Cfg::BM * 4 : 0);
   const int per_cu = std::max(1, std::min(160 * 1024 / lds, Cfg::kWavesPerSimd * 4 / Cfg::NW));
   const int64_t most = (int64_t)device_cu_count() * per_cu;
   const unsigned grid = (unsigned)std::min<int64_t>((tiles + kMxXcds - 1) / kMxXcds * kMxXcds, most);

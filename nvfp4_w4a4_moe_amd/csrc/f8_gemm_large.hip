@@ -1,5 +1,5 @@
-// FP8 grouped GEMM, 256-row tiles: 256 x 256 on the FP8 instruction, 256 x 128 on converted codes and where
-// every weight row has its own scale (whose registers do not last for more).
+// FP8 grouped GEMM, 256-row tiles: 256 x 256 on the FP8 instruction, 256 x 128 on converted codes (whose registers
+// do not last for more).
 #include "f8_gemm_kernel.h"
 
 namespace nv4 {
@@ -7,9 +7,6 @@ namespace nv4 {
 hipError_t launch_f8_gemm_large(const F8GemmArgs &g, hipStream_t stream) {
   typedef F8Tile<4, 2, 2, 4, 2, 2> Square;
   typedef F8Tile<4, 2, 2, 2, 2, 2> Half;
-  if (g.group_mode == NV4_GROUP_K)
-    return g.c_is_f32 ? f8_launch<Half, NV4_GROUP_K, NV4_EPI_NONE, true>(g, stream)
-                      : f8_launch<Half, NV4_GROUP_K, NV4_EPI_NONE, false>(g, stream);
   if (g.epilogue != NV4_EPI_SWIGLU)
     return g.c_is_f32 ? f8_launch<Half, NV4_GROUP_M, NV4_EPI_NONE, true>(g, stream)
                       : f8_launch<Square, NV4_GROUP_M, NV4_EPI_NONE, false>(g, stream);

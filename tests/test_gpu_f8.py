@@ -342,10 +342,13 @@ def test_swiglu_requantised_in_the_epilogue(gpu_lib, counts, N, rule):
         C = torch.empty((R, N + 8), dtype=ct, device="cuda")[:, :N]
         gpu_lib.fp8_grouped_gemm(aq, bq, dev_i32(off), E, N, C=C, q_out=part, rule=rule, **o)
         if ct == torch.float32:
-            assert same_bits(C.contiguous(), plain)
-            check_codes(part, host(plain), rule)
+            # (small problems without q_out take another kernel, with another order of the sum over K)
+            assert R < 1000 or same_bits(C.contiguous(), plain)
+            check_product(host(C), vals(aq), tile_vals(bq), off, E, N, swiglu=True)
+            check_codes(part, host(C.contiguous()), rule)
         else:
-            assert same_bits(C.contiguous(), gpu_lib.fp8_grouped_gemm(aq, bq, dev_i32(off), E, N, out_dtype=ct, **o))
+            assert R < 1000 or same_bits(C.contiguous(), gpu_lib.fp8_grouped_gemm(aq, bq, dev_i32(off), E, N, out_dtype=ct, **o))
+            check_product(host(C), vals(aq), tile_vals(bq), off, E, N, swiglu=True, bf16=True)
             # the codes of a result that is itself between two BF16 values: half a BF16 step and half a code step
             v, c = vals(part), host(C).astype(np.float64)
             G = np.repeat(host(part.scales).astype(np.float64), 128, 1)[:, :N]
