@@ -60,51 +60,109 @@ inline BalWs bal_ws(void *ws, int64_t T, int E, int nseg, size_t *bytes) {
   return w;
 }
 
+// Tokens that a half-wave (wave) loads at once: as the registers last, or one where tokens are few (257 tokens
+// of 60 experts, backward: 9.5 us with four, 4.9 with one; 65536 of 128, loss: 15.9 and 23).
+__host__ __device__ constexpr int bal_at(int npl, bool many) { return !many ? 1 : npl <= 4 ? 4 : npl <= 8 ? 2 : 1; }
+inline bool bal_many(int64_t T) { return T >= 16384; }
+
 // a segment border, inside [0, T] whatever the array holds
 __device__ __forceinline__ int64_t bal_border(const int32_t *off, int s, int64_t T) {
   return off ? std::min<int64_t>(std::max<int64_t>(off[s], 0), T) : s ? T : 0;
 }
-// the last segment that starts at or before t, -1 without one
-__device__ __forceinline__ int bal_segment(const int32_t *off, int nseg, int64_t t) {
-  if (!off) return 0;
-  int lo = -1, hi = nseg;  // off[lo] <= t < off[hi]
+// the last segment that starts at or before t, -1 without one: among lo .. hi, off[lo] <= t < off[hi]
+__device__ __forceinline__ int bal_segment(const int32_t *off, int lo, int hi, int64_t t) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (off[mid] <= t) lo = mid; else hi = mid;
   }
   return lo;
 }
-
-// One token's softmax on its LPT lanes: v[i] = exp(l - max) (0 behind E), their sum, and lse.  A token
-// whose logits are all -infinity has v = 0 and sum 0.
-template <int NPL, int LPT>
-__device__ __forceinline__ void bal_softmax(const float *lg, bool valid, int E, int ll, float (&v)[NPL], float &sum,
-                                            float &lse, bool &bad) {
-  float mx = -INFINITY;
-  bad = false;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = ll + LPT * i;
-    v[i] = -INFINITY;
-    if (valid && e < E) v[i] = lg[e];
-    bad |= !(v[i] < INFINITY);  // NaN or +infinity
-    mx = fmaxf(mx, v[i]);
+// The same by the whole wave for one t, 64 borders at a time: a load for 64 segments where halving would
+// take six, one behind the other.
+__device__ __forceinline__ int bal_segment_wave(const int32_t *off, int nseg, int64_t t) {
+  if (!off) return 0;
+  const int lane = threadIdx.x & 63;
+  int lo = -1, hi = nseg;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64, i = lo + (lane + 1) * step;
+    const int n = __popcll(__ballot(i < hi && off[min(i, nseg)] <= t));
+    const int next = lo + n * step;
+    hi = min(hi, next + step);
+    lo = next;
   }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// e^x for x <= 0 to two steps of FP32: the hardware's 2^y for y = x log2(e) rounded, times 1 + what the
+// rounding left.  Below 2^-126 it may be 0.
+__device__ __forceinline__ float bal_exp(float x) {
+  const float c = __builtin_elementwise_maximum(x, -104.0f);  // (a NaN stays)
+  const float y = c * 0x1.715476p+0f;
+  const float left = __builtin_fmaf(c, 0x1.4ae0cp-26f, __builtin_fmaf(c, 0x1.715476p+0f, -y));
+  const float r = __builtin_amdgcn_exp2f(y);
+  return __builtin_fmaf(r, left * 0x1.62e43p-1f, r);
+}
+
+// A token's logits on its LPT lanes: four consecutive ones of every 4 LPT on a lane where it has that
+// many, else every LPT-th
+template <int NPL, int LPT>
+__device__ __forceinline__ int bal_expert(int ll, int i) {
+  return NPL % 4 == 0 ? i / 4 * 4 * LPT + ll * 4 + i % 4 : ll + LPT * i;
+}
+// (-infinity behind E and where there is no token; wide: E and the array allow 16-byte loads)
+template <int NPL, int LPT, class T>
+__device__ __forceinline__ void bal_load(const T *row, bool valid, bool wide, int E, int ll, T none, T (&v)[NPL]) {
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) v[i] = none;
+  if (!valid) return;
+  if (NPL % 4 == 0 && wide) {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < NPL; i += 4) {
+      const int e = bal_expert<NPL, LPT>(ll, i);
+      if (e >= E) continue;
+      const T4 x = *reinterpret_cast<const T4 *>(row + e);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[(i + r) % NPL] = x[r];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = bal_expert<NPL, LPT>(ll, i);
+      if (e < E) v[i] = row[e];
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ bool bal_wide(const T *p, int E) {
+  return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// One token's softmax: v[i] = exp(l - max) in the logits' place, 1 / their sum, and lse.  A token whose logits
+// are all -infinity has v = 0 and inv = 0; a NaN or +infinity among them makes all three NaN.
+template <int NPL, int LPT>
+__device__ __forceinline__ void bal_softmax(float (&v)[NPL], float &inv, float &lse, bool &bad) {
+  float mx = v[0];
+#pragma unroll
+  for (int i = 1; i < NPL; ++i) mx = fmaxf(mx, v[i]);
   mx = wave_max_dpp<LPT>(mx);
-  const bool none = mx == -INFINITY;
-  sum = 0.0f;
+  mx = mx == -INFINITY ? 0.0f : mx;
+  float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    v[i] = none ? (v[i] != v[i] ? v[i] : 0.0f) : expf(v[i] - mx);
+    v[i] = bal_exp(v[i] - mx);
     sum += v[i];
   }
   sum = wave_sum_dpp<LPT>(sum);
+  bad = sum != sum;
   lse = sum == 0.0f ? 0.0f : mx + logf(sum);
+  inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
-template <int NPL, int LPT>
+template <int NPL, int LPT, bool MANY>
 __global__ __launch_bounds__(kBalThreads) void k_balance(BalanceArgs a, BalWs w, int64_t chunk) {
   constexpr int TPW = 64 / LPT, TPB = kBalWaves * TPW;  // tokens at a time
+  constexpr int AT = bal_at(NPL, MANY);                  // times as many under way
   __shared__ int cnt[kMaxE];
   __shared__ float ps[kBalWaves][NPL * LPT];
   __shared__ float zs[kBalWaves][2];
@@ -112,7 +170,8 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(BalanceArgs a, BalWs w,
   if (blockIdx.x == 0 && tid == 0) *w.done = 0;
   const int64_t end = std::min<int64_t>((blockIdx.x + 1) * chunk, a.T);
   int64_t t = blockIdx.x * chunk;
-  int s = bal_segment(a.seg_offsets, a.nseg, t);
+  int s = bal_segment_wave(a.seg_offsets, a.nseg, t);
+  const bool wide = bal_wide(a.logits, a.E);
   bool bad = false, badid = false;
   if (s < 0) {
     s = 0;
@@ -128,24 +187,32 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(BalanceArgs a, BalWs w,
     int n = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) acc[i] = 0.0f;
-    for (int64_t t0 = t; t0 < hi; t0 += TPB) {  // (the same count for every wave)
-      const int64_t tt = t0 + wave * TPW + sub;
-      const bool live = tt < hi && (!a.mask || a.mask[tt]);
-      float v[NPL], sum, lse;
-      bool b;
-      bal_softmax<NPL, LPT>(a.logits + tt * a.E, live, a.E, ll, v, sum, lse, b);
-      if (!live) continue;
-      bad |= b;
-      if (sum != 0.0f) {
+    for (int64_t t0 = t; t0 < hi; t0 += AT * TPB) {  // (the same count for every wave)
+      float v[AT][NPL];
+      int id[AT];
+      bool live[AT];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) acc[i] += v[i] / sum;
-        z = __builtin_fmaf(lse, lse, z);
+      for (int u = 0; u < AT; ++u) {
+        const int64_t tt = t0 + u * TPB + wave * TPW + sub;
+        bal_load<NPL, LPT>(a.logits + tt * a.E, tt < hi, wide, a.E, ll, -INFINITY, v[u]);
+        live[u] = tt < hi && (!a.mask || a.mask[tt]);
+        id[u] = tt < hi && ll < a.k ? a.topk_ids[tt * a.k + ll] : 0;
       }
-      ++n;
-      if (ll < a.k) {
-        const int id = a.topk_ids[tt * a.k + ll];
-        if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1);
-        else badid = true;
+#pragma unroll
+      for (int u = 0; u < AT; ++u) {
+        float inv, lse;
+        bool b;
+        bal_softmax<NPL, LPT>(v[u], inv, lse, b);
+        if (!live[u]) continue;
+        bad |= b;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) acc[i] = __builtin_fmaf(v[u][i], inv, acc[i]);
+        z = __builtin_fmaf(lse, lse, z);
+        ++n;
+        if (ll < a.k) {
+          if (id[u] >= 0 && id[u] < a.E) atomicAdd(&cnt[id[u]], 1);
+          else badid = true;
+        }
       }
     }
     // the wave's two tokens, then the waves
@@ -157,7 +224,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(BalanceArgs a, BalWs w,
     }
     if (sub == 0) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) ps[wave][ll + LPT * i] = acc[i];
+      for (int i = 0; i < NPL; ++i) ps[wave][bal_expert<NPL, LPT>(ll, i)] = acc[i];
     }
     if (lane == 0) zs[wave][0] = z, zs[wave][1] = __int_as_float(n);
     __syncthreads();
@@ -185,59 +252,61 @@ __global__ __launch_bounds__(kBalThreads) void k_balance(BalanceArgs a, BalWs w,
   }
 }
 
-// One workgroup of 1024 a segment: its slots' sums, 16 at a time for 64 experts, and its losses; the
-// last workgroup adds the segments' losses.
+// One workgroup of 1024 a segment: its slots' sums, 1024 / P at a time (P: the power of two from E on, 64 at
+// least), and its losses; the last workgroup adds the segments' losses.
 __global__ __launch_bounds__(1024) void k_balance_sum(BalanceArgs a, BalWs w, int64_t chunk) {
-  __shared__ float sp[16][64];
-  __shared__ int sc[16][64];
+  __shared__ float sp[1024];
+  __shared__ int sc[1024];
   __shared__ float s_dot[16], s_z[16];
   __shared__ int s_n[16];
   __shared__ bool s_last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.x;
   const int64_t lo = bal_border(a.seg_offsets, s, a.T), hi = bal_border(a.seg_offsets, s + 1, a.T);
   const int64_t first = lo / chunk + s, last = hi > lo ? (hi - 1) / chunk + s : first - 1;
-  float dot = 0.0f;
-  for (int e0 = 0; e0 < a.E; e0 += 64) {
-    const int e = e0 + lane;
-    float p = 0.0f;
-    int c = 0;
-    if (e < a.E) {
-#pragma unroll 4
-      for (int64_t b = first + wave; b <= last; b += 16) {
-        p += w.psum[b * a.E + e];
-        c += w.count[b * a.E + e];
-      }
-    }
-    sp[wave][lane] = p;
-    sc[wave][lane] = c;
-    __syncthreads();
-    if (wave == 0 && e < a.E) {
-#pragma unroll
-      for (int i = 1; i < 16; ++i) p += sp[i][lane], c += sc[i][lane];
-      a.prob_sums[(int64_t)s * a.E + e] = p;
-      a.counts[(int64_t)s * a.E + e] = c;
-      dot = __builtin_fmaf((float)c, p, dot);
-    }
-    __syncthreads();
-  }
-  float z = 0.0f;
-  int n = 0;
+  const int P = a.E <= 64 ? 64 : 1 << (32 - __clz(a.E - 1)), e = tid & (P - 1), groups = 1024 / P;
+  float dot = 0.0f, p = 0.0f, z = 0.0f;
+  int c = 0, n = 0;
   for (int64_t b = first + tid; b <= last; b += 1024) z += w.z[b], n += w.n[b];
+  if (e < a.E) {
+#pragma unroll 8
+    for (int64_t b = first + tid / P; b <= last; b += groups) {
+      p += w.psum[b * a.E + e];
+      c += w.count[b * a.E + e];
+    }
+  }
+  sp[tid] = p;
+  sc[tid] = c;
+  __syncthreads();
+  if (tid < a.E) {  // (P >= E: the first group's threads)
+#pragma unroll 4
+    for (int i = 1; i < groups; ++i) p += sp[i * P + tid], c += sc[i * P + tid];
+    a.prob_sums[(int64_t)s * a.E + tid] = p;
+    a.counts[(int64_t)s * a.E + tid] = c;
+    dot = (float)c * p;
+  }
   z = wave_sum_dpp(z);
   n = (int)wave_reduce_u32((uint32_t)n, [](uint32_t x, uint32_t y) { return x + y; });
   dot = wave_sum_dpp(dot);
   if (lane == 0) s_dot[wave] = dot, s_z[wave] = z, s_n[wave] = n;
   __syncthreads();
   if (tid == 0) {
-    z = s_z[0], n = s_n[0];
-    for (int i = 1; i < 16; ++i) z += s_z[i], n += s_n[i];
+    dot = s_dot[0], z = s_z[0], n = s_n[0];
+    for (int i = 1; i < 16; ++i) dot += s_dot[i], z += s_z[i], n += s_n[i];
     a.tokens[s] = n;
     // (n^2 as FP32 factors: 65536 tokens squared leave 32 bits)
     const float fn = (float)n;
-    w.seg[2 * s] = n ? (float)a.E / (float)a.k / fn * (s_dot[0] / fn) : 0.0f;
-    w.seg[2 * s + 1] = n ? z / fn : 0.0f;
-    __threadfence();
-    s_last = atomicAdd(w.done, 1u) == (uint32_t)a.nseg - 1u;
+    const float bal = n ? (float)a.E / (float)a.k / fn * (dot / fn) : 0.0f;
+    const float zz = n ? z / fn : 0.0f;
+    s_last = false;
+    if (a.nseg == 1) {
+      a.loss[0] = bal;
+      a.loss[1] = zz;
+    } else {
+      w.seg[2 * s] = bal;
+      w.seg[2 * s + 1] = zz;
+      __threadfence();
+      s_last = atomicAdd(w.done, 1u) == (uint32_t)a.nseg - 1u;
+    }
   }
   __syncthreads();
   if (!s_last) return;
@@ -263,80 +332,151 @@ __global__ __launch_bounds__(1024) void k_balance_sum(BalanceArgs a, BalWs w, in
 // The gradient of a token's logits on its LPT lanes.  With q_j = sum of dw_m over the choices m of expert
 // j and m_j how many there are, the weights' part is p_j (q_j - sum_i p_i q_i), or with renormalised
 // weights r_j = p_j / sum_i m_i p_i:  r_j (q_j - m_j sum_i r_i q_i).
-template <int NPL, int LPT>
+template <int NPL, int LPT, bool MANY, bool RENORM>
 __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwardArgs a) {
-  constexpr int TPW = 64 / LPT;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane / LPT, ll = lane % LPT;
-  const int64_t t = ((int64_t)blockIdx.x * kBalWaves + wave) * TPW + sub;
-  const bool valid = t < a.T;
-  float dw = 0.0f;
-  int id = -1;
-  if (valid && a.dtopk_w && ll < a.k) {
-    dw = a.dtopk_w[t * a.k + ll];
-    id = a.topk_ids[t * a.k + ll];
-    if (id < 0 || id >= a.E) {
-      id = -1;
+  constexpr int TPW = 64 / LPT, AT = bal_at(NPL, MANY);
+  const int lane = threadIdx.x & 63, sub = lane / LPT, ll = lane % LPT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ volatile int places[kBalWaves][TPW][NPL * LPT];
+  // AT times TPW consecutive tokens a wave
+  const int64_t first = ((int64_t)blockIdx.x * kBalWaves + wave) * (AT * TPW);
+  if (first >= a.T) return;
+  const int64_t last = std::min<int64_t>(first + AT * TPW, a.T) - 1;
+  const bool wide = bal_wide(a.logits, a.E), wide_c = bal_wide(a.counts, a.E), wide_d = bal_wide(a.dlogits, a.E);
+  float l[AT][NPL], dw[AT];
+  int id[AT];
+  bool counted[AT];
+#pragma unroll
+  for (int u = 0; u < AT; ++u) {
+    const int64_t t = first + u * TPW + sub;
+    const bool valid = t < a.T;
+    bal_load<NPL, LPT>(a.logits + t * a.E, valid, wide, a.E, ll, -INFINITY, l[u]);
+    dw[u] = 0.0f;
+    id[u] = -1;
+    if (valid && a.dtopk_w && ll < a.k) {
+      dw[u] = a.dtopk_w[t * a.k + ll];
+      id[u] = a.topk_ids[t * a.k + ll];
+    }
+    counted[u] = valid && a.dloss && (!a.mask || a.mask[t]);
+  }
+  // a segment's coefficients: of p_j (c_j - sum) and of lse p_j
+  const auto coefficients = [&](int s, float &cb, float &cz) {
+    const float n = s >= 0 ? (float)a.tokens[s] : 0.0f;
+    cb = n > 0.0f ? a.dloss[0] * ((float)a.E / (float)a.k / (float)a.nseg / n) / n : 0.0f;
+    cz = n > 0.0f ? a.dloss[1] * 2.0f / (float)a.nseg / n : 0.0f;
+    return n > 0.0f;
+  };
+  int s0 = 0, s1 = 0;
+  float cb0 = 0.0f, cz0 = 0.0f;
+  bool any0 = false;
+  int64_t end0 = 0;
+  if (a.dloss) {
+    s0 = bal_segment_wave(a.seg_offsets, a.nseg, first);
+    s1 = !a.seg_offsets || (s0 >= 0 && s0 + 1 < a.nseg && last < a.seg_offsets[s0 + 1]) || s0 == a.nseg - 1
+             ? s0 : bal_segment_wave(a.seg_offsets, a.nseg, last);
+    end0 = bal_border(a.seg_offsets, s0 + 1, a.T);
+    any0 = coefficients(s0, cb0, cz0);
+  }
+#pragma unroll
+  for (int u = 0; u < AT; ++u) {
+    const int64_t t = first + u * TPW + sub;
+    const bool valid = t < a.T;
+    if (id[u] < -1 || id[u] >= a.E || (id[u] == -1 && valid && a.dtopk_w && ll < a.k)) {
       if (a.dev_status) atomicOr(a.dev_status, kDsBadExpert);
+      id[u] = -1;
+      dw[u] = 0.0f;
     }
-  }
-  bool counted = valid && a.dloss && (!a.mask || a.mask[t]);
-  int s = 0;
-  float fn = 0.0f;
-  if (counted) {
-    s = bal_segment(a.seg_offsets, a.nseg, t);
-    counted = s >= 0 && t < bal_border(a.seg_offsets, s + 1, a.T);
-    if (counted) fn = (float)a.tokens[s];
-    counted = counted && fn > 0.0f;
-  }
-  // whether the weights' gradient reaches the token: some dw that is not 0 (NaN included)
-  const uint64_t any = __ballot(!(dw == 0.0f));
-  const bool weighted = LPT == 64 ? any != 0 : (uint32_t)(any >> (32 * sub)) != 0;
-  const bool live = counted || weighted;
-  float v[NPL], sum, lse;
-  bool bad;
-  bal_softmax<NPL, LPT>(a.logits + t * a.E, live, a.E, ll, v, sum, lse, bad);
-  if (bad && live && a.dev_status) atomicOr(a.dev_status, kDsNanLogit);
-  float cb = 0.0f, cz = 0.0f;
-  if (counted) {
-    cb = a.dloss[0] * ((float)a.E / (float)a.k / (float)a.nseg / fn) / fn;
-    cz = a.dloss[1] * 2.0f / (float)a.nseg / fn * lse;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  float c[NPL], q[NPL], m[NPL], cp = 0.0f, pq = 0.0f, mp = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = ll + LPT * i;
-    v[i] *= inv;
-    c[i] = counted && e < a.E ? (float)a.counts[(int64_t)s * a.E + e] : 0.0f;
-    q[i] = m[i] = 0.0f;
-    cp = __builtin_fmaf(c[i], v[i], cp);
-  }
-  if (a.dtopk_w) {
-    for (int j = 0; j < a.k; ++j) {
-      const int idj = __shfl(id, sub * LPT + j, 64);
-      const float dwj = __shfl(dw, sub * LPT + j, 64);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (idj == ll + LPT * i) q[i] += dwj, m[i] += 1.0f;
+    int s = s0;
+    float cb = cb0, cz = cz0;
+    bool in = any0;
+    int64_t end = end0;
+    if (s1 != s0 && counted[u]) {
+      s = bal_segment(a.seg_offsets, s0, s1 + 1, t);
+      end = bal_border(a.seg_offsets, s + 1, a.T);
+      in = coefficients(s, cb, cz);
     }
+    in = in && counted[u] && t < end;
+    float c[NPL], cf[NPL];
+    int ci[NPL];
+    bal_load<NPL, LPT>(a.counts + (int64_t)max(s, 0) * a.E, in, wide_c, a.E, ll, 0, ci);
+    // whether the weights' gradient reaches the token: some dw that is not 0 (NaN included)
+    const uint64_t any = __ballot(!(dw[u] == 0.0f));
+    const bool weighted = LPT == 64 ? any != 0 : (uint32_t)(any >> (32 * sub)) != 0;
+    const bool live = in || weighted;
+    float (&v)[NPL] = l[u];
+    float inv, lse;
+    bool bad;
+    bal_softmax<NPL, LPT>(v, inv, lse, bad);
+    if (bad && live && a.dev_status) atomicOr(a.dev_status, kDsNanLogit);
+    cb = in ? cb : 0.0f;
+    cz = in ? cz * lse : 0.0f;
+    float q[NPL], m[NPL], cp = 0.0f, pq = 0.0f, mp = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      pq = __builtin_fmaf(v[i], q[i], pq);
-      mp = __builtin_fmaf(v[i], m[i], mp);
+      v[i] *= inv;
+      c[i] = (float)ci[i];
+      q[i] = m[i] = 0.0f;
+      cp = __builtin_fmaf(c[i], v[i], cp);
     }
-    pq = wave_sum_dpp<LPT>(pq);
-    if (a.renorm) mp = wave_sum_dpp<LPT>(mp);
-  }
-  cp = wave_sum_dpp<LPT>(cp);
-  const float rz = a.renorm ? (mp == 0.0f ? 0.0f : 1.0f / mp) : 1.0f, D = pq * rz;
-  if (!valid) return;
+    if (a.dtopk_w) {
+      // Choice j leaves j + 1 in its expert's place, and the experts' lanes fetch what they find there.  (A
+      // choice that does not find its own has the same expert as another one: those are compared one by one.)
+      volatile __attribute__((address_space(3))) int *place =  // (a wave's LDS accesses keep their order)
+          (volatile __attribute__((address_space(3))) int *)places[wave][sub];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = ll + LPT * i;
-    if (e >= a.E) continue;
-    float d = v[i] * __builtin_fmaf(cb, c[i] - cp, cz);
-    if (weighted) d = __builtin_fmaf(v[i] * rz, q[i] - (a.renorm ? m[i] * D : D), d);
-    a.dlogits[t * a.E + e] = live ? d : 0.0f;
+      for (int i = 0; i < NPL; ++i) place[bal_expert<NPL, LPT>(ll, i)] = 0;
+      if (id[u] >= 0) place[id[u]] = ll + 1;
+      const bool twice = id[u] >= 0 && place[id[u]] != ll + 1;
+      if (__ballot(twice) == 0) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          const int j = place[bal_expert<NPL, LPT>(ll, i)];
+          const float dwj = __shfl(dw[u], sub * LPT + max(j - 1, 0), 64);
+          q[i] = j ? dwj : 0.0f;
+          m[i] = j ? 1.0f : 0.0f;
+        }
+      } else for (int j = 0; j < a.k; ++j) {
+        const int idj = __shfl(id[u], sub * LPT + j, 64);
+        const float dwj = __shfl(dw[u], sub * LPT + j, 64);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          const bool hit = idj == bal_expert<NPL, LPT>(ll, i);
+          q[i] += hit ? dwj : 0.0f;
+          if (RENORM) m[i] += hit ? 1.0f : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        pq = __builtin_fmaf(v[i], q[i], pq);
+        if (RENORM) mp = __builtin_fmaf(v[i], m[i], mp);
+      }
+      pq = wave_sum_dpp<LPT>(pq);
+      if (RENORM) mp = wave_sum_dpp<LPT>(mp);
+    }
+    cp = wave_sum_dpp<LPT>(cp);
+    const float rz = RENORM ? (mp == 0.0f ? 0.0f : 1.0f / mp) : 1.0f, D = pq * rz;
+    if (!valid) continue;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      float d = v[i] * __builtin_fmaf(cb, c[i] - cp, cz);
+      if (weighted) d = __builtin_fmaf(v[i] * rz, q[i] - (RENORM ? m[i] * D : D), d);
+      cf[i] = live ? d : 0.0f;
+    }
+    float *out = a.dlogits + t * a.E;
+    if (NPL % 4 == 0 && wide_d) {
+#pragma unroll
+      for (int i = 0; i < NPL; i += 4) {
+        const int e = bal_expert<NPL, LPT>(ll, i);
+        if (e < a.E)
+          *reinterpret_cast<f32x4 *>(out + e) = f32x4{cf[i], cf[(i + 1) % NPL], cf[(i + 2) % NPL], cf[(i + 3) % NPL]};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int e = bal_expert<NPL, LPT>(ll, i);
+        if (e < a.E) out[e] = cf[i];
+      }
+    }
   }
 }
 
@@ -365,7 +505,9 @@ hipError_t launch_balance_loss(const BalanceArgs &a, hipStream_t stream) {
   // (without a token one workgroup still clears the count of finished segments)
   const unsigned grid = (unsigned)std::max<int64_t>(bal_chunks(a.T), 1);
   by_experts(a.E, [&](auto npl, auto lpt) {
-    k_balance<decltype(npl)::value, decltype(lpt)::value><<<grid, kBalThreads, 0, stream>>>(a, w, chunk);
+    constexpr int N = decltype(npl)::value, L = decltype(lpt)::value;
+    if (bal_many(a.T)) k_balance<N, L, true><<<grid, kBalThreads, 0, stream>>>(a, w, chunk);
+    else k_balance<N, L, false><<<grid, kBalThreads, 0, stream>>>(a, w, chunk);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -376,9 +518,14 @@ hipError_t launch_balance_loss(const BalanceArgs &a, hipStream_t stream) {
 hipError_t launch_balance_backward(const BalanceBackwardArgs &a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   by_experts(a.E, [&](auto npl, auto lpt) {
-    constexpr int tokens = kBalWaves * 64 / decltype(lpt)::value;
-    k_balance_backward<decltype(npl)::value, decltype(lpt)::value>
-        <<<(unsigned)((a.T + tokens - 1) / tokens), kBalThreads, 0, stream>>>(a);
+    constexpr int N = decltype(npl)::value, L = decltype(lpt)::value;
+    const bool many = bal_many(a.T), renorm = a.renorm && a.dtopk_w;
+    const int tokens = kBalWaves * 64 / L * bal_at(N, many);
+    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    if (many && renorm) k_balance_backward<N, L, true, true><<<grid, kBalThreads, 0, stream>>>(a);
+    else if (many) k_balance_backward<N, L, true, false><<<grid, kBalThreads, 0, stream>>>(a);
+    else if (renorm) k_balance_backward<N, L, false, true><<<grid, kBalThreads, 0, stream>>>(a);
+    else k_balance_backward<N, L, false, false><<<grid, kBalThreads, 0, stream>>>(a);
   });
   return hipGetLastError();
 }

@@ -2,8 +2,9 @@
 //   dY[token_row[t][j]] = w[t][j] dout[t],   dw[t][j] = sum_h dout[t][h] Y[token_row[t][j]][h].
 //
 // Memory bound: a token's row of dout is read, k rows of Y read and k rows of dY written.  One workgroup a
-// token; every thread owns 4 consecutive columns and keeps a partial dot product for each of up to eight
-// choices at a time.
+// token; every thread owns V consecutive columns (16 bytes of a row of Y, or 8 of BF16 where rows start between
+// 16-byte steps) and keeps a partial dot product for each of up to eight choices at a time, whose loads are all
+// under way together.
 #include "nv4_device.h"
 #include "nv4_internal.h"
 #include "router_internal.h"
@@ -14,30 +15,40 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAtOnce = 8;
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-template <bool F32>
-__device__ __forceinline__ f32x4 load4(const void *p, int64_t at) {
-  if constexpr (F32) {
-    return __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + at));
-  } else {
-    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(static_cast<const uint16_t *>(p) + at));
-    return f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
-                 __uint_as_float(v[1] & 0xFFFF0000u)};
+// V values of a row as they are in memory, and as FP32
+template <bool F32, int V>
+struct Cols {
+  typedef uint32_t Words __attribute__((ext_vector_type(F32 ? 4 : V / 2)));
+  static constexpr int N = F32 ? V / 4 : 1;
+  Words w[N];
+  __device__ __forceinline__ void load(const void *p, int64_t at) {
+    const Words *q = reinterpret_cast<const Words *>(static_cast<const char *>(p) + at * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __builtin_nontemporal_load(q + i);
   }
-}
-template <bool F32>
-__device__ __forceinline__ void store4(void *p, int64_t at, f32x4 v) {
-  if constexpr (F32) {
-    __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(static_cast<float *>(p) + at));
-  } else {
-    __builtin_nontemporal_store(u32x2{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                                      f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)},
-                                reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at));
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i / 4][i % 4]);
+    else return __uint_as_float(i % 2 ? w[0][i / 2] & 0xFFFF0000u : w[0][i / 2] << 16);
   }
-}
+  // d times s, each product rounded to the type
+  template <class D>
+  __device__ __forceinline__ void store(void *p, int64_t at, const D &d, float s) {
+    Words *q = reinterpret_cast<Words *>(static_cast<char *>(p) + at * (F32 ? 4 : 2));
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i / 4][i % 4] = __float_as_uint(d.get(i) * s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2)
+        w[0][i / 2] = f32_to_bf16_rne(d.get(i) * s) | (f32_to_bf16_rne(d.get(i + 1) * s) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) __builtin_nontemporal_store(w[i], q + i);
+  }
+};
 
-template <bool DOUT_F32, bool Y_F32>
+template <bool DOUT_F32, bool Y_F32, int V>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineBackwardArgs a) {
   __shared__ float sums[kThreads / 64][kAtOnce];
   const int64_t t = blockIdx.x;
@@ -53,17 +64,25 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineBackwardAr
       w[j] = j < nj ? a.topk_w[t * a.k + j0 + j] : 0.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t c = (int64_t)tid * 4; c < a.H; c += kThreads * 4) {
-      const f32x4 d = load4<DOUT_F32>(a.dout, t * a.H + c);
+    for (int64_t c = (int64_t)tid * V; c < a.H; c += kThreads * V) {
+      Cols<DOUT_F32, V> d;
+      Cols<Y_F32, V> y[kAtOnce];
+      d.load(a.dout, t * a.H + c);
+      if (a.dtopk_w) {
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        if (row[j] < 0) continue;  // uniform
-        if (a.dtopk_w) {
-          const f32x4 y = load4<Y_F32>(a.Y, row[j] * a.ldy + c);
+        for (int j = 0; j < kAtOnce; ++j)
+          if (row[j] >= 0) y[j].load(a.Y, row[j] * a.ldy + c);  // (the same for the workgroup)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dot[j] = __builtin_fmaf(d[i], y[i], dot[j]);
+        for (int j = 0; j < kAtOnce; ++j) {
+          if (row[j] < 0) continue;
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(d.get(i), y[j].get(i), dot[j]);
         }
-        if (a.dY) store4<Y_F32>(a.dY, row[j] * a.lddy + c, d * w[j]);
+      }
+      if (a.dY) {
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+          if (row[j] >= 0) y[j].store(a.dY, row[j] * a.lddy + c, d, w[j]);
       }
     }
     if (a.dtopk_w) {
@@ -84,19 +103,23 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineBackwardAr
   }
 }
 
+template <bool DOUT_F32, bool Y_F32, int V>
+hipError_t launch(const CombineBackwardArgs &a, hipStream_t stream) {
+  k_combine_backward<DOUT_F32, Y_F32, V><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_combine_backward(const CombineBackwardArgs &a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  const unsigned grid = (unsigned)a.T;
-  if (a.dout_is_f32) {
-    if (a.y_is_f32) k_combine_backward<true, true><<<grid, kThreads, 0, stream>>>(a);
-    else k_combine_backward<true, false><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    if (a.y_is_f32) k_combine_backward<false, true><<<grid, kThreads, 0, stream>>>(a);
-    else k_combine_backward<false, false><<<grid, kThreads, 0, stream>>>(a);
-  }
-  return hipGetLastError();
+  if (a.y_is_f32) return a.dout_is_f32 ? launch<true, true, 4>(a, stream) : launch<false, true, 4>(a, stream);
+  // 16-byte accesses where every row that is touched allows them
+  const auto steps = [](const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; };
+  const bool wide = a.H % 8 == 0 && (a.dout_is_f32 || steps(a.dout, a.H)) && (!a.dtopk_w || steps(a.Y, a.ldy)) &&
+                    (!a.dY || steps(a.dY, a.lddy));
+  if (wide) return a.dout_is_f32 ? launch<true, false, 8>(a, stream) : launch<false, false, 8>(a, stream);
+  return a.dout_is_f32 ? launch<true, false, 4>(a, stream) : launch<false, false, 4>(a, stream);
 }
 
 }  // namespace nv4
