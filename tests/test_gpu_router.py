@@ -266,3 +266,77 @@ def test_combine_backward_is_moe_combines(gpu_lib):
         base = np.abs(host(dY) * vy).sum() + np.abs(host(dw) * vw).sum()
         assert abs(f(vy.astype(np.float32), w) - (host(dY) * vy).sum()) <= base * 2.0 ** -20
         assert abs(f(Y, vw.astype(np.float32)) - (host(dw) * vw).sum()) <= (base + np.abs(Y).sum() * 4) * 2.0 ** -20
+
+
+@pytest.mark.parametrize("T,k,H", [(3, 2, 8), (17, 8, 2048), (5, 9, 264), (33, 3, 4096), (2, 12, 8184)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_combine_backward_of_aligned_bf16_rows(gpu_lib, T, k, H, dt):
+    """Rows that allow 16-byte accesses give the bits that rows between such steps give."""
+    r = synth.rng(H)
+    dout = torch.from_numpy(r.standard_normal((T, H)).astype(np.float32)).to(dt).cuda()
+    Y = torch.from_numpy(r.standard_normal((T * k, H)).astype(np.float32)).bfloat16().cuda()
+    row, w = dev_i32(r.permutation(T * k).reshape(T, k)), dev_f32(r.random((T, k), dtype=np.float32))
+    dY, dw = gpu_lib.moe_combine_backward(dout, Y, row, w)
+    ry, rw = R.combine_backward(host(dout), host(Y), host(row), host(w))
+    assert (np.abs(host(dY) - ry) <= (2.0 ** -24 + 2.0 ** -8) * np.abs(ry)).all()
+    mag = R.combine_backward(np.abs(host(dout)), np.abs(host(Y)), host(row), host(w))[1]
+    assert (np.abs(host(dw) - rw) <= H * HALF * mag).all()
+    between = torch.zeros(T * k, H + 4, dtype=torch.bfloat16, device="cuda")[:, 4:]
+    between.copy_(Y)
+    y2, w2 = gpu_lib.moe_combine_backward(dout, between, row, w)
+    assert same_bits(y2.contiguous(), dY) and (np.abs(host(w2) - rw) <= H * HALF * mag).all()
+
+
+# ----------------------------------------------------------------------------- many tokens
+
+def many(T, E, k, seed):
+    """Logits a good deal apart, choices by size (the first of a few tokens twice), a mask, and segments whose
+    borders lie inside a wave's tokens, some of them empty."""
+    r = synth.rng(seed)
+    l = (3 * r.standard_normal((T, E))).astype(np.float32)
+    ids = np.argsort(-l, 1, kind="stable")[:, :k].astype(np.int32)
+    if k > 1:
+        ids[5::97, 1] = ids[5::97, 0]
+    mask = r.random(T) < 0.9
+    off = np.sort(np.concatenate([[0, 3, 3, 5, T - 2], r.integers(0, T, 20), [T]])).astype(np.int32)
+    return l, ids, mask, off, r
+
+
+@pytest.mark.parametrize("T,E,k", [(16384, 7, 2), (16391, 60, 4), (20001, 128, 8), (16400, 130, 8), (16385, 260, 3), (16389, 600, 8)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_many_tokens(gpu_lib, T, E, k, renorm):
+    l, ids, mask, off, r = many(T, E, k, T + E)
+    dw = r.standard_normal((T, k)).astype(np.float32)
+    dw[::3] = 0
+    check(gpu_lib, l, ids, mask, off, np.array([0.7, 0.3], np.float32), dw, renorm)
+
+
+@pytest.mark.parametrize("T", [40, 16390])
+def test_arrays_between_16_byte_steps(gpu_lib, T):
+    """The same bits where the arrays' starts do not allow wide accesses."""
+    E, k = 128, 4
+    l, ids, mask, off, r = many(T, E, k, 9)
+    so, m, idd, dl = dev_i32(off), dev_mask(mask), dev_i32(ids), dev_f32(np.array([0.5, 2], np.float32))
+    dw = dev_f32(r.standard_normal((T, k)).astype(np.float32))
+    lg = dev_f32(l)
+    odd = torch.empty(T * E + 1, device="cuda")[1:].view(T, E)
+    odd.copy_(lg)
+    a, b = [gpu_lib.moe_balance_loss(x, idd, mask=m, seg_offsets=so) for x in (lg, odd)]
+    assert all(same_bits(x, y) for x, y in zip(vars(a).values(), vars(b).values()))
+    run = lambda x, **o: gpu_lib.moe_balance_backward(x, idd, a, dl, dtopk_w=dw, mask=m, seg_offsets=so, **o)
+    g = run(lg)
+    assert same_bits(run(odd, out=torch.empty(T * E + 1, device="cuda")[1:].view(T, E)), g)
+    assert same_bits(run(odd, out=odd), g)
+    a.counts = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), a.counts.flatten()])[1:].view_as(a.counts)
+    assert same_bits(run(lg), g)
+
+
+def test_many_empty_segments(gpu_lib):
+    """65536 segments, most of them empty, for a few tokens and for many."""
+    for T in (100, 16500):
+        r = synth.rng(T)
+        E, k, n = 8, 2, 65536
+        l = r.standard_normal((T, E)).astype(np.float32)
+        ids = np.argsort(-l, 1)[:, :k].astype(np.int32)
+        off = np.sort(np.concatenate([[0], r.integers(0, T, n - 1), [T]])).astype(np.int32)
+        check(gpu_lib, l, ids, None, off, np.array([500.0, 300.0], np.float32), None, False)
