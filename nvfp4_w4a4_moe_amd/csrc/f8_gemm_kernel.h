@@ -402,8 +402,14 @@ void k_f8_gemm(F8GemmArgs g) {
       constexpr int PER = 16 / ESZ, G = OUT_F32 || NF > 1 ? 4 : 2, FRAGS = G / ESZ;
       const int gl = lane & (G - 1);
       const int col_g = col_w + (gl / ESZ) * 32 + h * 16 + (gl % ESZ) * PER;  // this lane's piece of a group's first fragment
-      const bool dwords = OUT_F32 || ((int64_t)reinterpret_cast<uintptr_t>(g.C) | g.ldc * ESZ) % 4 == 0;
-      const bool ragged = !dwords || (ncols % PER != 0 && col_w + NF * 32 > ncols);
+      // Rows that start between lines: the parts of a line are put together in L2 and not streamed (8 x 2500 rows of
+      // 2047 FP32 columns, K = 720: 122 -> 85 us).  BF16 rows that start between dwords are no buffer's to store.  Where
+      // registers are short for this (256 x 256 tiles), and under SwiGLU, whose columns are a multiple of 32, such
+      // rows are streamed or stored one value at a time.
+      constexpr bool ANY = !SWIGLU && FM * FN < 8;
+      const int64_t starts = (int64_t)reinterpret_cast<uintptr_t>(g.C) | g.ldc * ESZ;
+      const bool lines = !ANY || starts % 64 == 0, dwords = OUT_F32 || starts % 4 == 0;
+      const bool ragged = (!ANY && !dwords) || (ncols % PER != 0 && col_w + NF * 32 > ncols);
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
 #pragma unroll
@@ -424,9 +430,16 @@ void k_f8_gemm(F8GemmArgs g) {
 #pragma unroll
           for (int k = 0; k < G; ++k) {
             const uint32_t at = (uint32_t)((f * 32 + (l32 & ~(G - 1)) + k) * ldc + col) * ESZ;
-            const bool piece = dwords && col + PER <= ncols;
-            __builtin_amdgcn_raw_buffer_store_b128(c[k], dst, piece ? at : kNoStore, 0, kStream);
-            if (ragged) {  // one by one: the piece over the last column, and rows that start between dwords
+            const bool piece = (ANY || dwords) && col + PER <= ncols;
+            if (lines) {
+              __builtin_amdgcn_raw_buffer_store_b128(c[k], dst, piece ? at : kNoStore, 0, kStream);
+            } else if (dwords) {
+              __builtin_amdgcn_raw_buffer_store_b128(c[k], dst, piece ? at : kNoStore, 0, 0);
+            } else if (piece && f * 32 + (l32 & ~(G - 1)) + k < rows) {
+              typedef f8_u32x4 Anywhere __attribute__((aligned(2)));
+              *reinterpret_cast<Anywhere *>(cb + at) = c[k];
+            }
+            if (ragged) {  // one by one
 #pragma unroll
               for (int r = 0; r < PER; ++r) {
                 const uint32_t v = !piece && col + r < ncols ? at + r * ESZ : kNoStore;
