@@ -330,6 +330,37 @@ __global__ __launch_bounds__(1024) void k_balance_sum(BalanceArgs a, BalWs w, in
   }
 }
 
+// A token's row in LDS, this lane's experts of it: a wave's own accesses to LDS keep their order, and volatile ones
+// the program's.
+template <class T>
+using LdsRow = volatile __attribute__((address_space(3))) T *;
+template <int NPL, int LPT, class T>
+__device__ __forceinline__ void bal_clear_row(LdsRow<T> row, int ll) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  if constexpr (NPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += 4) *(LdsRow<T4>)(row + bal_expert<NPL, LPT>(ll, i)) = T4{0, 0, 0, 0};
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) row[bal_expert<NPL, LPT>(ll, i)] = 0;
+  }
+}
+template <int NPL, int LPT, class T>
+__device__ __forceinline__ void bal_read_row(LdsRow<T> row, int ll, T (&v)[NPL]) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  if constexpr (NPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += 4) {
+      const T4 x = *(LdsRow<T4>)(row + bal_expert<NPL, LPT>(ll, i));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[i + r] = x[r];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = row[bal_expert<NPL, LPT>(ll, i)];
+  }
+}
+
 // The gradient of a token's logits on its LPT lanes.  With q_j = sum of dw_m over the choices m of expert
 // j and m_j how many there are, the weights' part is p_j (q_j - sum_i p_i q_i), or with renormalised
 // weights r_j = p_j / sum_i m_i p_i:  r_j (q_j - m_j sum_i r_i q_i).
@@ -338,7 +369,10 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
   constexpr int TPW = 64 / LPT, AT = bal_at(NPL, MANY);
   const int lane = threadIdx.x & 63, sub = lane / LPT, ll = lane % LPT;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  __shared__ volatile int places[kBalWaves][TPW][NPL * LPT];
+  __shared__ __attribute__((aligned(16))) int places[kBalWaves][TPW][NPL * LPT];
+  __shared__ __attribute__((aligned(16))) float weights[kBalWaves][TPW][NPL * LPT];
+  const LdsRow<int> place = (LdsRow<int>)places[wave][sub];
+  const LdsRow<float> weight = (LdsRow<float>)weights[wave][sub];
   // AT times TPW consecutive tokens a wave
   const int64_t first = ((int64_t)blockIdx.x * kBalWaves + wave) * (AT * TPW);
   if (first >= a.T) return;
@@ -378,6 +412,15 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
     end0 = bal_border(a.seg_offsets, s0 + 1, a.T);
     any0 = coefficients(s0, cb0, cz0);
   }
+  // counts of the segment that all of the wave's tokens lie in
+  float c[NPL];
+  int ci[NPL];
+  const auto load_counts = [&](int s, bool in) {
+    bal_load<NPL, LPT>(a.counts + (int64_t)max(s, 0) * a.E, in, wide_c, a.E, ll, 0, ci);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) c[i] = (float)ci[i];
+  };
+  load_counts(s0, any0 && s1 == s0);
 #pragma unroll
   for (int u = 0; u < AT; ++u) {
     const int64_t t = first + u * TPW + sub;
@@ -397,9 +440,8 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
       in = coefficients(s, cb, cz);
     }
     in = in && counted[u] && t < end;
-    float c[NPL], cf[NPL];
-    int ci[NPL];
-    bal_load<NPL, LPT>(a.counts + (int64_t)max(s, 0) * a.E, in, wide_c, a.E, ll, 0, ci);
+    if (s1 != s0) load_counts(s, in);
+    float cf[NPL];
     // whether the weights' gradient reaches the token: some dw that is not 0 (NaN included)
     const uint64_t any = __ballot(!(dw[u] == 0.0f));
     const bool weighted = LPT == 64 ? any != 0 : (uint32_t)(any >> (32 * sub)) != 0;
@@ -415,26 +457,26 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       v[i] *= inv;
-      c[i] = (float)ci[i];
       q[i] = m[i] = 0.0f;
       cp = __builtin_fmaf(c[i], v[i], cp);
     }
     if (a.dtopk_w) {
-      // Choice j leaves j + 1 in its expert's place, and the experts' lanes fetch what they find there.  (A
-      // choice that does not find its own has the same expert as another one: those are compared one by one.)
-      volatile __attribute__((address_space(3))) int *place =  // (a wave's LDS accesses keep their order)
-          (volatile __attribute__((address_space(3))) int *)places[wave][sub];
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) place[bal_expert<NPL, LPT>(ll, i)] = 0;
-      if (id[u] >= 0) place[id[u]] = ll + 1;
+      // A choice leaves its weight's gradient with its expert, whose lane fetches it.  (One that does not find its own
+      // lane in the expert's place has the same expert as another one: those are compared one by one.)
+      bal_clear_row<NPL, LPT, float>(weight, ll);
+      if (RENORM) bal_clear_row<NPL, LPT, int>(place, ll);
+      if (id[u] >= 0) {
+        place[id[u]] = ll + 1;
+        weight[id[u]] = dw[u];
+      }
       const bool twice = id[u] >= 0 && place[id[u]] != ll + 1;
       if (__ballot(twice) == 0) {
+        bal_read_row<NPL, LPT, float>(weight, ll, q);
+        if (RENORM) {
+          int j[NPL];
+          bal_read_row<NPL, LPT, int>(place, ll, j);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          const int j = place[bal_expert<NPL, LPT>(ll, i)];
-          const float dwj = __shfl(dw[u], sub * LPT + max(j - 1, 0), 64);
-          q[i] = j ? dwj : 0.0f;
-          m[i] = j ? 1.0f : 0.0f;
+          for (int i = 0; i < NPL; ++i) m[i] = j[i] ? 1.0f : 0.0f;
         }
       } else for (int j = 0; j < a.k; ++j) {
         const int idj = __shfl(id[u], sub * LPT + j, 64);
@@ -457,10 +499,11 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
     cp = wave_sum_dpp<LPT>(cp);
     const float rz = RENORM ? (mp == 0.0f ? 0.0f : 1.0f / mp) : 1.0f, D = pq * rz;
     if (!valid) continue;
+    const float base = __builtin_fmaf(-cb, cp, cz) - (!RENORM && weighted ? D : 0.0f);
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      float d = v[i] * __builtin_fmaf(cb, c[i] - cp, cz);
-      if (weighted) d = __builtin_fmaf(v[i] * rz, q[i] - (RENORM ? m[i] * D : D), d);
+      float d = v[i] * (RENORM ? __builtin_fmaf(cb, c[i], base) : __builtin_fmaf(cb, c[i], base) + q[i]);
+      if (RENORM && weighted) d = __builtin_fmaf(v[i] * rz, q[i] - m[i] * D, d);
       cf[i] = live ? d : 0.0f;
     }
     float *out = a.dlogits + t * a.E;

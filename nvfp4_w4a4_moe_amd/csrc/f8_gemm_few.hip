@@ -39,10 +39,10 @@ __device__ __forceinline__ f32x4 few_product(const FewBlock &w, const FewBlock &
 }
 
 // The expert and first row of row tile `slot` (tiles of 16 rows, in the experts' order), by every wave for
-// itself; false if there are fewer.  Offsets below zero or decreasing are taken as empty.
+// itself; false if there are fewer.  Offsets below zero or decreasing are taken as empty, those behind M_cap as M_cap.
 __device__ __forceinline__ bool few_tile(const F8GemmArgs &g, int slot, int &e, int &m0, int &m_end) {
   const int lane = threadIdx.x & 63, per = (g.E + 63) / 64;
-  const auto off = [&](int i) { return max(g.offsets[min(i, g.E)], 0); };
+  const auto off = [&](int i) { return min(max(g.offsets[min(i, g.E)], 0), (int)g.M_cap); };
   const auto tiles = [&](int lo, int hi) { return (max(hi - lo, 0) + kRows - 1) / kRows; };
   int own = 0;
   for (int i = 0; i < per; ++i) {
@@ -59,16 +59,17 @@ __device__ __forceinline__ bool few_tile(const F8GemmArgs &g, int slot, int &e, 
   if (behind == 0) return false;
   const int l = __ffsll((unsigned long long)behind) - 1;  // the lane whose experts have it
   int left = slot - __builtin_amdgcn_readlane(run - own, l);
-  for (e = l * per;; ++e) {
+  for (e = l * per; e < g.E; ++e) {
     m0 = off(e);
     m_end = off(e + 1);
     const int n = tiles(m0, m_end);
-    if (left < n) break;
+    if (left < n) {
+      m0 += left * kRows;
+      return true;
+    }
     left -= n;
   }
-  m0 += left * kRows;
-  m_end = min(m_end, (int)g.M_cap);
-  return m0 < m_end;
+  return false;
 }
 
 // four consecutive columns of a row

@@ -200,8 +200,10 @@ void k_f8_gemm(F8GemmArgs g) {
   const int64_t b_srows = K_GROUPS ? g.b_rows : (b_rows + 127) / 128;
   const uint32_t b_bytes = (uint32_t)(b_rows * g.K), b_sbytes = (uint32_t)(b_srows * sld);
 
-  // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty)
-  for (int e = tid; e <= g.E; e += NT) off[e] = std::max(g.offsets[e], 0);
+  // ---- tile space (offsets below zero or decreasing are outside the contract: taken as empty; behind the last row: as
+  // that)
+  const int most = K_GROUPS ? (int)g.K : (int)g.M_cap;
+  for (int e = tid; e <= g.E; e += NT) off[e] = std::min(std::max(g.offsets[e], 0), most);
   __syncthreads();
   MxTiles<Cfg, GROUP, EPI, F8GemmArgs> tiles{g, off, tab, 0, 0, 0, 0, 0, 0};
   tiles_setup(g, off, tab, reinterpret_cast<int *>(ring), tiles);
