@@ -77,18 +77,19 @@ __device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
   return i32x4{(int)p, (int)(p >> 32) & 0xFFFF, (int)bytes, 0x00020000};
 }
 template <bool STREAM>
-__device__ __forceinline__ void f8_dma16(i32x4 buffer, uint32_t lds, uint32_t voff) {
+__device__ __forceinline__ void f8_dma16(i32x4 buffer, uint32_t lds, uint32_t voff, uint32_t soff) {
   if (STREAM)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(voff),
-                 "s"(buffer)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(voff),
+                 "s"(buffer), "s"(soff)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff),
-                 "s"(buffer)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+                 "s"(buffer), "s"(soff)
                  : "memory");
 }
-__device__ __forceinline__ void f8_dma4(i32x4 buffer, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buffer)
+__device__ __forceinline__ void f8_dma4(i32x4 buffer, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+               "s"(buffer), "s"(soff)
                : "memory");
 }
 __device__ __forceinline__ uint32_t f8_lds(const void *p) {
@@ -210,6 +211,8 @@ void k_f8_gemm(F8GemmArgs g) {
   // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included)
   uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
   const int qrow = lane >> 3, qpos = lane & 7;  // row and ring position in a code DMA
+  static_assert(Cfg::NW % 2 == 0, "the chunk there is the same in all of a wave's");
+  const int chunk = f8_swz(qpos, wave * 8 + qrow);
   MxJob pj{};     // the loading tile (the loads are up to kStages tiles ahead of the products, and leave them here)
   int4(&queue)[kQueue] = jobs[wave];
   int p_it = -1;  // its number in this workgroup's sequence
@@ -227,7 +230,7 @@ void k_f8_gemm(F8GemmArgs g) {
     const auto one = [&](int r, int *dst) MX_INLINE {
       const int row = j.m0 + (r - BN);
       f8_dma4(f8_buffer(g.a_rows_index, (uint32_t)g.M_cap * 4u), f8_lds(dst),
-              r >= BN && r < BN + BM && row < j.m_end ? (uint32_t)row * 4u : kNoRow);
+              r >= BN && r < BN + BM && row < j.m_end ? (uint32_t)row * 4u : kNoRow, 0);
     };
 #pragma unroll
     for (int l = 0; l < Cfg::kLook; ++l) one(code_row(l), rows_c[wave] + l * 64);
@@ -257,7 +260,7 @@ void k_f8_gemm(F8GemmArgs g) {
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
       const int row = __shfl(mc[i / 8], (i * 8 + qrow) & 63, 64);
-      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(f8_swz(qpos, (i * Cfg::NW + wave) * 8 + qrow) * 16);
+      off_c[i] = row < 0 ? kNoRow : (uint32_t)row * ld + (uint32_t)(chunk * 16);
     }
 #pragma unroll
     for (int l = 0; l < Cfg::kScaleDma; ++l) {
@@ -300,27 +303,29 @@ void k_f8_gemm(F8GemmArgs g) {
     if (part == 0) {
       if (p_live && (p_it < 0 || p_st == pj.nst)) next_tile();
       l_k0 = (uint32_t)(pj.k_lo + p_st * 128);
-      l_left = p_live ? (int)g.K - (int)l_k0 : 0;  // elements behind k0 (may exceed the block)
+      l_left = (int)g.K - (int)l_k0;  // elements behind k0 (may exceed the block)
       ++p_st;
     }
-    const i32x4 buffer_a = f8_buffer(g.a_codes, a_bytes), buffer_b = f8_buffer(b_codes, b_bytes);
+    // (with nothing to load, buffers of no bytes; an absent row's offset is behind the buffer under any l_k0, and so are the
+    // chunks behind K)
+    const uint32_t some = p_live ? ~0u : 0u;
+    const i32x4 buffer_a = f8_buffer(g.a_codes, a_bytes & some), buffer_b = f8_buffer(b_codes, b_bytes & some);
+    const bool in_k = chunk * 16 < l_left;
 #pragma unroll
     for (int i = 0; i < Cfg::kCodeDma; ++i) {
       if (i * parts / Cfg::kCodeDma != part) continue;
       const int b = i * Cfg::NW + wave;
-      const bool in_k = f8_swz(qpos, b * 8 + qrow) * 16 < l_left;
-      // (saturating: without a row the sum stays behind the buffer)
-      const uint32_t v = in_k ? __builtin_elementwise_add_sat(off_c[i], l_k0) : kNoRow;
-      if (i >= Cfg::kDmaB) f8_dma16<false>(buffer_a, dst + b * 1024, v);
-      else f8_dma16<Cfg::kStreamB>(buffer_b, dst + b * 1024, v);
+      const uint32_t v = in_k ? off_c[i] : kNoRow;
+      if (i >= Cfg::kDmaB) f8_dma16<false>(buffer_a, dst + b * 1024, v, l_k0);
+      else f8_dma16<Cfg::kStreamB>(buffer_b, dst + b * 1024, v, l_k0);
     }
     if (part == parts - 1) {
 #pragma unroll
       for (int l = 0; l < Cfg::kScaleDma; ++l) {
         const int b = wave * Cfg::kScaleDma + l;
-        const uint32_t v = l_left > 0 ? __builtin_elementwise_add_sat(off_s[l], l_k0 / 128 * 4) : kNoRow;
         const bool of_b = b * 64 < BN;
-        f8_dma4(f8_buffer(of_b ? b_scales : g.a_scales, of_b ? b_sbytes : a_sbytes), dst + Cfg::kScaleBase + b * 256, v);
+        f8_dma4(f8_buffer(of_b ? b_scales : g.a_scales, (of_b ? b_sbytes : a_sbytes) & some),
+                dst + Cfg::kScaleBase + b * 256, off_s[l], l_k0 / 128 * 4);
       }
     }
   };
@@ -339,37 +344,36 @@ void k_f8_gemm(F8GemmArgs g) {
   float sa[FM], sb[MANY ? 16 : 1], nb[MANY ? 16 : 1];
   const int w_row = wn * FN * 32, t_row = BN + wm * FM * 32;
   // LDS addresses are integers: slots, fragments and rows differ by multiples of 128, the chunks of a row by the low
-  // bits that the swizzle permutes
-  const uint32_t lane_at = (uint32_t)(l32 * 128 + f8_swz(h * 4, l32) * 16);
-  const auto raw = [&](uint32_t st, int row0) MX_INLINE {
-    const uint32_t at = lane_at + (st + row0 * 128);
-    F8Raw r;
+  // bits that the swizzle permutes.  at[q]: chunk q of this lane's row of the wave's first weight fragment, in the slot
+  // being read.
+  uint32_t at[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r.c[q] = *f8_lds_ptr<i32x4>(at ^ (q * 16));
-    return r;
+  for (int q = 0; q < 4; ++q) at[q] = ring_at + (uint32_t)((w_row + l32) * 128 + (f8_swz(h * 4, l32) ^ q) * 16);
+  const auto read_tokens = [&](int f) MX_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tr[f].c[q] = *f8_lds_ptr<i32x4>(at[q] + (uint32_t)(t_row - w_row) * 128 + f * 4096);
   };
-  const auto read_tokens = [&](uint32_t st, int f) MX_INLINE { tr[f] = raw(st, t_row + f * 32); };
   const auto read_scales = [&](uint32_t st) MX_INLINE {
 #pragma unroll
     for (int f = 0; f < FM; ++f) sa[f] = *f8_lds_ptr<float>(st + Cfg::kScaleBase + (t_row + f * 32 + l32) * 4);
   };
   // weight fragment i and its scales (into nb)
   const auto read_weights = [&](uint32_t st, int i) MX_INLINE {
-    const int row0 = w_row + i * 32;
-    wr = raw(st, row0);
-    const uint32_t at = st + Cfg::kScaleBase + row0 * 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) wr.c[q] = *f8_lds_ptr<i32x4>(at[q] + i * 4096);
+    const uint32_t sc = st + Cfg::kScaleBase + (w_row + i * 32) * 4;
     if constexpr (POW2) {
-      nb[0] = *f8_lds_ptr<float>(at + l32 * 4);
+      nb[0] = *f8_lds_ptr<float>(sc + l32 * 4);
     } else if constexpr (K_GROUPS) {
       // register r: operand row 8 (r / 4) + 4 h + r % 4
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f32x4 t = *f8_lds_ptr<f32x4>(at + 8 * q * 4 + 4 * h * 4);
+        const f32x4 t = *f8_lds_ptr<f32x4>(sc + 8 * q * 4 + 4 * h * 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) nb[4 * q + r] = t[r];
       }
     } else {
-      nb[0] = *f8_lds_ptr<float>(at);  // a fragment's 32 rows lie in one block of 128
+      nb[0] = *f8_lds_ptr<float>(sc);  // a fragment's 32 rows lie in one block of 128
     }
   };
 
@@ -557,6 +561,8 @@ void k_f8_gemm(F8GemmArgs g) {
     mx_barrier();
   };
   const auto turn = [&]() MX_INLINE {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] += (uint32_t)(next_slot - slot);
     slot = next_slot;
     next_slot = next_slot == (S - 1) * Cfg::kStageBytes ? 0 : next_slot + Cfg::kStageBytes;
   };
@@ -581,7 +587,7 @@ void k_f8_gemm(F8GemmArgs g) {
       if (cj.nst > 0) {
         read_weights(ring_at + slot, 0);
 #pragma unroll
-        for (int f = 0; f < FM; ++f) read_tokens(ring_at + slot, f);
+        for (int f = 0; f < FM; ++f) read_tokens(f);
         read_scales(ring_at + slot);
       }
       if constexpr (NP == 2) {  // nothing waits yet
@@ -618,7 +624,7 @@ void k_f8_gemm(F8GemmArgs g) {
             if (i < SPREAD && st > 0) load_part(done, (i + 1) * FM + f, PARTS);
             if (i == FN - 1) {
               load_part(done, f, PARTS);
-              read_tokens(ring_at + slot, f);
+              read_tokens(f);
             }
             __builtin_amdgcn_sched_barrier(0);
           }
