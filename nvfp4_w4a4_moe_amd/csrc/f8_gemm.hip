@@ -36,10 +36,7 @@ hipError_t launch_f8_gemm(const F8GemmArgs &g, hipStream_t stream) {
     return (((g.M_cap + bm - 1) / bm + (g.E - 1) / 2) * ((n + bn - 1) / bn) + cus - 1) / cus;
   };
   const bool wide = g.c_is_f32, broad = g.q_codes;
-  // (256 x 256 tiles have no registers left for stores of BF16 rows that start between lines: 8 x 2500 rows of 2047
-  // columns, K = 720: 125 against 58, of 2044: 80 against 60; a longer K makes up for it)
-  const bool between = !wide && g.C && !swiglu && (reinterpret_cast<uintptr_t>(g.C) | (uintptr_t)g.ldc * 2) % 64 != 0;
-  if (!(between && g.K <= 1024) && g.M_cap >= 144 * (int64_t)g.E && !(wide && broad) &&
+  if (g.M_cap >= 144 * (int64_t)g.E && !(wide && broad) &&
       rounds(256, wide ? 128 : 256) * (wide ? 18 : 34) <= rounds(128, broad ? 256 : 128) * (broad ? 20 : 10))
     return launch_f8_gemm_large(g, stream);
   return launch_f8_gemm_medium(g, stream);

@@ -144,11 +144,11 @@ void k_f8_gemm_few(F8GemmArgs g) {
     float ts, ws[F];
   } st[kAhead];
   const auto load = [&](Stage &s, int b) MX_INLINE {
-    const int k = b * 128 + part * 16;
-    const bool lo = k < (int)g.K, hi = k + 64 < (int)g.K;
+    const uint32_t k = (uint32_t)b * 128 + part * 16;
+    const bool lo = k < (uint32_t)g.K, hi = k + 64 < (uint32_t)g.K;
     // (saturating: without a row the sum stays behind the buffer)
-    const auto at = [&](uint32_t base, bool in, int kk) MX_INLINE {
-      return in ? __builtin_elementwise_add_sat(base, (uint32_t)kk) : kAbsent;
+    const auto at = [&](uint32_t base, bool in, uint32_t kk) MX_INLINE {
+      return in ? __builtin_elementwise_add_sat(base, kk) : kAbsent;
     };
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -157,7 +157,7 @@ void k_f8_gemm_few(F8GemmArgs g) {
     }
     s.t.lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(codes_a, at(at_a, lo, k), 0, 0));
     s.t.hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(codes_a, at(at_a, hi, k + 64), 0, 0));
-    s.ts = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales_a, at(at_sa, b < blocks, b * 4), 0, 0));
+    s.ts = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(scales_a, at(at_sa, b < blocks, (uint32_t)b * 4), 0, 0));
 #pragma unroll
     for (int f = 0; f < F; ++f) s.ws[f] = b < blocks ? scales_b[f][b] : 0.0f;
   };

@@ -45,11 +45,13 @@
 namespace nv4 {
 namespace {
 
-// WAVES_M x WAVES_N waves of FM x FN 32 x 32 fragments; a ring of STAGES stages of one block (K = 128)
-template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES, int WAVES_PER_SIMD>
+// WAVES_M x WAVES_N waves of FM x FN 32 x 32 fragments; a ring of STAGES stages of one block (K = 128).  ANY_ROWS: made
+// for rows of C that start between lines too, which takes registers.
+template <int WAVES_M, int WAVES_N, int FM, int FN, int STAGES, int WAVES_PER_SIMD, bool ANY_ROWS = (FM * FN < 8)>
 struct F8Tile {
   static constexpr int kWavesM = WAVES_M, kWavesN = WAVES_N, kFM = FM, kFN = FN;
   static constexpr int kStages = STAGES, kWavesPerSimd = WAVES_PER_SIMD;
+  static constexpr bool kAnyRows = ANY_ROWS;
   static constexpr int NW = WAVES_M * WAVES_N, NT = NW * 64;
   static constexpr int BM = WAVES_M * FM * 32;  // rows of A (tokens)
   static constexpr int BN = WAVES_N * FN * 32;  // rows of B (weights)
@@ -413,10 +415,10 @@ void k_f8_gemm(F8GemmArgs g) {
       const int gl = lane & (G - 1);
       const int col_g = col_w + (gl / ESZ) * 32 + h * 16 + (gl % ESZ) * PER;  // this lane's piece of a group's first fragment
       // Rows that start between lines: the parts of a line are put together in L2 and not streamed (8 x 2500 rows of
-      // 2047 FP32 columns, K = 720: 122 -> 85 us).  BF16 rows that start between dwords are no buffer's to store.  Where
-      // registers are short for this (256 x 256 tiles), and under SwiGLU, whose columns are a multiple of 32, such
-      // rows are streamed or stored one value at a time.
-      constexpr bool ANY = !SWIGLU && FM * FN < 8;
+      // 2047 FP32 columns, K = 720: 122 -> 85 us).  BF16 rows that start between dwords are no buffer's to store.
+      // Tiles that are not made for such rows, and SwiGLU's, whose columns are a multiple of 32, stream them or store
+      // them one value at a time.
+      constexpr bool ANY = !SWIGLU && Cfg::kAnyRows;
       const int64_t starts = (int64_t)reinterpret_cast<uintptr_t>(g.C) | g.ldc * ESZ;
       const bool lines = !ANY || starts % 64 == 0, dwords = OUT_F32 || starts % 4 == 0;
       const bool ragged = (!ANY && !dwords) || (ncols % PER != 0 && col_w + NF * 32 > ncols);
