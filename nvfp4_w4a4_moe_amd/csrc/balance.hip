@@ -6,7 +6,7 @@
 //
 // A logit is 4 bytes read (backward: and 4 written), an exp and some twenty other operations, so that both
 // passes are bound by the VALU before memory.  65536 tokens of 128 experts: loss 15 us (VALU busy 67 %, 2.4 TB/s), the
-// segments' sums 13, backward 25 (89 %, 2.8 TB/s).
+// segments' sums 13, backward 23 (84 %, 3.0 TB/s).
 //
 // Loss: a workgroup takes a chunk of consecutive tokens, a half-wave (or wave) a token at a time, each
 // lane summing its own experts' probabilities in registers over the tokens; where a segment ends inside

@@ -30,8 +30,8 @@ hipError_t launch_f8_gemm(const F8GemmArgs &g, hipStream_t stream) {
   if (g.M_cap <= 64 * (int64_t)g.E) return launch_f8_gemm_small(g, stream);
   // 256-row tiles from about 144 rows per expert (192 rows each: 131 against 141, 128: 109 against 97) where the rounds
   // of tiles on the CUs, an expert's last tile half full in the mean, come out cheaper: a 256 x 256 tile takes 3.4 times
-  // a 128 x 128 tile's share of a CU, a 256 x 128 tile with FP32 results 1.8 times (8192^3: 507 against 689, FP32 919
-  // against 1020; 8192 x 2048 x 768, 96 large tiles: 34 against 24; 4096^3, 256 of them: 71 against 91).
+  // a 128 x 128 tile's share of a CU, a 256 x 128 tile with FP32 results 1.8 times (8192^3: 527 against 699, FP32 930
+  // against 1049; 8192 x 2048 x 768, 96 large tiles: 34 against 24; 4096^3, 256 of them: 71 against 91).
   const auto rounds = [&](int64_t bm, int64_t bn) {
     return (((g.M_cap + bm - 1) / bm + (g.E - 1) / 2) * ((n + bn - 1) / bn) + cus - 1) / cus;
   };

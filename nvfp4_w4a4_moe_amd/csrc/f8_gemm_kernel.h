@@ -28,9 +28,10 @@
 // slot just read is refilled.  Every stage issues the same number of loads (a load with nothing to fetch has
 // an offset behind the buffer), so a wait counts exactly what may still be under way.
 //
-// 8192^3: 515 us or 2130 TFLOP/s (by the clock, 2010 to 2170), power-of-two scales 2130 to 2450, FP32 results 1160.  Gate
-// and up of 131072 rows with SwiGLU (128 experts, K 2048, 768 columns): 455 us, 1810 TFLOP/s, with MFMA busy 43 % of
-// the cycles, the sums' multiply-adds and addresses 49 %, and LDS reading 24 KB for 16 MFMA of a wave.
+// 8192^3: 527 us or 2085 TFLOP/s (by the clock, 1970 to 2090), power-of-two scales 2130 to 2200, FP32 results 1185.  Gate
+// and up of 131072 rows with SwiGLU (128 experts, K 2048, 768 columns): 436 us, 1890 TFLOP/s.  What bounds it: MFMA is
+// busy 44 % of the cycles, the VALU (the sums' multiply-adds, addresses) 45 %, hardly both at once, and LDS reads 24
+// KB for 16 MFMA of a wave, as long as they take.
 #pragma once
 
 #include <algorithm>
