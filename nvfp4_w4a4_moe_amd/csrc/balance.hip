@@ -363,7 +363,9 @@ __device__ __forceinline__ void bal_read_row(LdsRow<T> row, int ll, T (&v)[NPL])
 
 // The gradient of a token's logits on its LPT lanes.  With q_j = sum of dw_m over the choices m of expert
 // j and m_j how many there are, the weights' part is p_j (q_j - sum_i p_i q_i), or with renormalised
-// weights r_j = p_j / sum_i m_i p_i:  r_j (q_j - m_j sum_i r_i q_i).
+// weights r_j = p_j / sum_i m_i p_i:  r_j (q_j - m_j sum_i r_i q_i).  Where no choice has the row's largest logit
+// that sum may leave FP32's range: r_j is then taken from the choices' own softmax, exp(l_j - the largest chosen
+// logit).  The logits are read again for it, by the few waves that meet such a token.
 template <int NPL, int LPT, bool MANY, bool RENORM>
 __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwardArgs a) {
   constexpr int TPW = 64 / LPT, AT = bal_at(NPL, MANY);
@@ -453,11 +455,11 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
     if (bad && live && a.dev_status) atomicOr(a.dev_status, kDsNanLogit);
     cb = in ? cb : 0.0f;
     cz = in ? cz * lse : 0.0f;
-    float q[NPL], m[NPL], cp = 0.0f, pq = 0.0f, mp = 0.0f;
+    float q[NPL], m[NPL], r[NPL], cp = 0.0f, pq = 0.0f, mp = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       v[i] *= inv;
-      q[i] = m[i] = 0.0f;
+      q[i] = m[i] = r[i] = 0.0f;
       cp = __builtin_fmaf(c[i], v[i], cp);
     }
     if (a.dtopk_w) {
@@ -488,10 +490,31 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
           if (RENORM) m[i] += hit ? 1.0f : 0.0f;
         }
       }
+      if (RENORM) {
+        bool largest = false;  // (exp of the largest logit is 1, its probability inv)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          r[i] = v[i];
+          largest |= m[i] != 0.0f && v[i] == inv;
+        }
+        const uint64_t found = __ballot(largest);
+        const bool far = weighted && (LPT == 64 ? found == 0 : (uint32_t)(found >> (32 * sub)) == 0);
+        if (__ballot(far) != 0) {
+          float x[NPL], mx = -INFINITY;
+          bal_load<NPL, LPT>(a.logits + t * a.E, valid, wide, a.E, ll, -INFINITY, x);
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) mx = fmaxf(mx, m[i] != 0.0f ? x[i] : -INFINITY);
+          mx = wave_max_dpp<LPT>(mx);
+          mx = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i)
+            if (far) r[i] = m[i] != 0.0f ? bal_exp(x[i] - mx) : 0.0f;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        pq = __builtin_fmaf(v[i], q[i], pq);
-        if (RENORM) mp = __builtin_fmaf(v[i], m[i], mp);
+        pq = __builtin_fmaf(RENORM ? r[i] : v[i], q[i], pq);
+        if (RENORM) mp = __builtin_fmaf(r[i], m[i], mp);
       }
       pq = wave_sum_dpp<LPT>(pq);
       if (RENORM) mp = wave_sum_dpp<LPT>(mp);
@@ -503,7 +526,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       float d = v[i] * (RENORM ? __builtin_fmaf(cb, c[i], base) : __builtin_fmaf(cb, c[i], base) + q[i]);
-      if (RENORM && weighted) d = __builtin_fmaf(v[i] * rz, q[i] - m[i] * D, d);
+      if (RENORM && weighted) d = __builtin_fmaf(r[i] * rz, q[i] - m[i] * D, d);
       cf[i] = live ? d : 0.0f;
     }
     float *out = a.dlogits + t * a.E;
