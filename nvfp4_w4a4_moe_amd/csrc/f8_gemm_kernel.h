@@ -74,7 +74,10 @@ struct F8Tile {
 // LDS DMA as mx_dma16 and mx_dma4, in assembly: a builtin's load into the ring makes the compiler wait for every load
 // in flight before the next LDS read that it cannot tell apart from it, which is most of them (the waits and
 // barriers here are placed by hand).  lds: the wave's LDS byte address.  No register is written but m0, which
-// nothing else in these kernels uses.
+// nothing else in these kernels uses (the compiler takes it for its own: it can't be named as clobbered).
+// A buffer load may read a scalar register five wait states after a vector instruction has written it, and the
+// operands here often come straight from a lane read, where scalars are kept: the compiler puts such waits before loads
+// of its own only, so m0's move and the nop are five.
 __device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   return i32x4{(int)p, (int)(p >> 32) & 0xFFFF, (int)bytes, 0x00020000};
@@ -82,16 +85,16 @@ __device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
 template <bool STREAM>
 __device__ __forceinline__ void f8_dma16(i32x4 buffer, uint32_t lds, uint32_t voff, uint32_t soff) {
   if (STREAM)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(voff),
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(voff),
                  "s"(buffer), "s"(soff)
                  : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
                  "s"(buffer), "s"(soff)
                  : "memory");
 }
 __device__ __forceinline__ void f8_dma4(i32x4 buffer, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
                "s"(buffer), "s"(soff)
                : "memory");
 }
