@@ -214,8 +214,12 @@ void k_f8_gemm(F8GemmArgs g) {
   __syncthreads();
   MxTiles<Cfg, GROUP, EPI, F8GemmArgs> tiles{g, off, tab, 0, 0, 0, 0, 0, 0};
   tiles_setup(g, off, tab, reinterpret_cast<int *>(ring), tiles);
-  // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included)
+  // ---- loads: this lane's byte offsets of the loading tile's rows (K offset not included).  Without a tile there are none.
   uint32_t off_c[Cfg::kCodeDma], off_s[Cfg::kScaleDma];
+#pragma unroll
+  for (int i = 0; i < Cfg::kCodeDma; ++i) off_c[i] = kNoRow;
+#pragma unroll
+  for (int l = 0; l < Cfg::kScaleDma; ++l) off_s[l] = kNoRow;
   const int qrow = lane >> 3, qpos = lane & 7;  // row and ring position in a code DMA
   static_assert(Cfg::NW % 2 == 0, "the chunk there is the same in all of a wave's");
   const int chunk = f8_swz(qpos, wave * 8 + qrow);
@@ -308,12 +312,13 @@ void k_f8_gemm(F8GemmArgs g) {
   const auto load_part = [&](uint32_t dst, int part, int parts) MX_INLINE {
     if (part == 0) {
       if (p_live && (p_it < 0 || p_st == pj.nst)) next_tile();
-      l_k0 = (uint32_t)(pj.k_lo + p_st * 128);
+      l_k0 = p_live ? (uint32_t)(pj.k_lo + p_st * 128) : 0u;
       l_left = (int)g.K - (int)l_k0;  // elements behind k0 (may exceed the block)
       ++p_st;
     }
-    // (with nothing to load, buffers of no bytes; an absent row's offset is behind the buffer under any l_k0, and so are the
-    // chunks behind K)
+    // (With nothing to load, buffers of no bytes and l_k0 = 0: the range check takes the scalar offset off the buffer's
+    // size, which may not fall below it.  An absent row's offset is behind the buffer under any l_k0, and so are the
+    // chunks behind K.)
     const uint32_t some = p_live ? ~0u : 0u;
     const i32x4 buffer_a = f8_buffer(g.a_codes, a_bytes & some), buffer_b = f8_buffer(b_codes, b_bytes & some);
     const bool in_k = chunk * 16 < l_left;
