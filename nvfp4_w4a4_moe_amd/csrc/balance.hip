@@ -16,6 +16,7 @@
 // workgroups run.
 #include <algorithm>
 
+#include "many_groups.h"
 #include "nv4_device.h"
 #include "nv4_internal.h"
 #include "router_internal.h"
@@ -376,7 +377,7 @@ __global__ __launch_bounds__(kBalThreads) void k_balance_backward(BalanceBackwar
   const LdsRow<int> place = (LdsRow<int>)places[wave][sub];
   const LdsRow<float> weight = (LdsRow<float>)weights[wave][sub];
   // AT times TPW consecutive tokens a wave
-  const int64_t first = ((int64_t)blockIdx.x * kBalWaves + wave) * (AT * TPW);
+  const int64_t first = ((int64_t)group_index() * kBalWaves + wave) * (AT * TPW);
   if (first >= a.T) return;
   const int64_t last = std::min<int64_t>(first + AT * TPW, a.T) - 1;
   const bool wide = bal_wide(a.logits, a.E), wide_c = bal_wide(a.counts, a.E), wide_d = bal_wide(a.dlogits, a.E);
@@ -588,7 +589,7 @@ hipError_t launch_balance_backward(const BalanceBackwardArgs &a, hipStream_t str
     constexpr int N = decltype(npl)::value, L = decltype(lpt)::value;
     const bool many = bal_many(a.T), renorm = a.renorm && a.dtopk_w;
     const int tokens = kBalWaves * 64 / L * bal_at(N, many);
-    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    const dim3 grid = many_groups((a.T + tokens - 1) / tokens);
     if (many && renorm) k_balance_backward<N, L, true, true><<<grid, kBalThreads, 0, stream>>>(a);
     else if (many) k_balance_backward<N, L, true, false><<<grid, kBalThreads, 0, stream>>>(a);
     else if (renorm) k_balance_backward<N, L, false, true><<<grid, kBalThreads, 0, stream>>>(a);

@@ -5,6 +5,7 @@
 // token; every thread owns V consecutive columns (16 bytes of a row of Y, or 8 of BF16 where rows start between
 // 16-byte steps) and keeps a partial dot product for each of up to eight choices at a time, whose loads are all
 // under way together.  16384 tokens of eight BF16 rows of 2048: 227 us, 5.0 TB/s (with 8-byte accesses 284).
+#include "many_groups.h"
 #include "nv4_device.h"
 #include "nv4_internal.h"
 #include "router_internal.h"
@@ -51,7 +52,8 @@ struct Cols {
 template <bool DOUT_F32, bool Y_F32, int V>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineBackwardArgs a) {
   __shared__ float sums[kThreads / 64][kAtOnce];
-  const int64_t t = blockIdx.x;
+  const int64_t t = group_index();
+  if (t >= a.T) return;
   const int tid = threadIdx.x;
   for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
     const int nj = min(a.k - j0, kAtOnce);
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineBackwardAr
 
 template <bool DOUT_F32, bool Y_F32, int V>
 hipError_t launch(const CombineBackwardArgs &a, hipStream_t stream) {
-  k_combine_backward<DOUT_F32, Y_F32, V><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
+  k_combine_backward<DOUT_F32, Y_F32, V><<<many_groups(a.T), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

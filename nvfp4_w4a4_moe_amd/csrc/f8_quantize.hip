@@ -15,6 +15,7 @@
 
 #include "f8_device.h"
 #include "f8_internal.h"
+#include "many_groups.h"
 #include "nv4_internal.h"
 #include "segment_tile.h"
 #include "../../include/nv4moe.h"
@@ -48,7 +49,7 @@ __device__ __forceinline__ bool f8_row_block(const uint4 (&v)[F32 ? 2 : 1], int 
 template <bool F32, int U>
 __global__ __launch_bounds__(256) void k_f8_rows(F8QuantArgs a, uint32_t units, uint32_t kb) {
   const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const uint32_t first = (blockIdx.x * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
+  const uint32_t first = (group_index() * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
   uint4 v[U][F32 ? 2 : 1];
   uint32_t row[U], blk[U], src[U];
 #pragma unroll
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(256) void k_f8_rows(F8QuantArgs a, uint32_t units, 
 // tile lies in one segment.  LDS row r keeps dword p of the tile at p ^ (16 * (r / 32 % 4)): the four
 // 32-row parts of a column, which neighbouring lanes read at once, then fall into different banks.
 template <bool F32, bool ROWS>
-__global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_cols(F8QuantArgs a, int chunks) {
+__global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_cols(F8QuantArgs a, int chunks, uint32_t n) {
   constexpr int NT = F32 ? 512 : 256, ES = F32 ? 4 : 2;
   constexpr int LPR = F32 ? 32 : 16;       // lanes of a row, 16 bytes each
   constexpr int W = LPR * 4;               // dwords of a tile row
@@ -103,8 +104,9 @@ __global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_cols(F8QuantArgs a, int 
   const int tid = threadIdx.x, lr = tid % LPR;
   // Each XCD (workgroup i runs on XCD i % 8) takes a contiguous share of the tiles, column tile by
   // column tile, so that with gathered rows it reads few columns of x.
-  const uint32_t n = gridDim.x, per = n / kXcds, full = per * kXcds;
-  const uint32_t L = blockIdx.x < full ? (blockIdx.x % kXcds) * per + blockIdx.x / kXcds : blockIdx.x;
+  const uint32_t b0 = group_index(), per = n / kXcds, full = per * kXcds;
+  if (b0 >= n) return;  // uniform
+  const uint32_t L = b0 < full ? (b0 % kXcds) * per + b0 / kXcds : b0;
   const uint32_t ct = L / (uint32_t)chunks, ch = L - ct * (uint32_t)chunks;
   const int64_t p0 = (int64_t)ch * 128;
   if (p0 >= a.seg_padded_offsets[a.nseg]) return;  // uniform
@@ -209,11 +211,13 @@ __global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_cols(F8QuantArgs a, int 
 
 // One 128 x 128 block of a matrix of m rows
 template <bool F32>
-__global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_tiles(F8QuantArgs a, uint32_t mb, uint32_t kb, int64_t m) {
+__global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_tiles(F8QuantArgs a, uint32_t mb, uint32_t kb, int64_t m, uint32_t n) {
   constexpr int NT = F32 ? 512 : 256, ES = F32 ? 4 : 2, LPR = F32 ? 32 : 16;
   __shared__ uint32_t s_max[NT / 64];
   const int tid = threadIdx.x, lr = tid % LPR;
-  const uint32_t ct = blockIdx.x % kb, rb = blockIdx.x / kb;  // rb: block row over all matrices
+  const uint32_t block = group_index();
+  if (block >= n) return;  // uniform
+  const uint32_t ct = block % kb, rb = block / kb;  // rb: block row over all matrices
   const uint32_t s = rb / mb;
   const int64_t in0 = (int64_t)(rb - s * mb) * 128, row0 = (int64_t)s * m + in0;
   const int64_t valid = m - in0, mycol = (int64_t)ct * 128 + lr * (16 / ES);
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(F32 ? 512 : 256) void k_f8_tiles(F8QuantArgs a, uin
     }
   }
   if (tid == 0) {
-    a.scales[blockIdx.x] = sc.G;
+    a.scales[block] = sc.G;
     if (sc.bad && a.dev_status) atomicOr(a.dev_status, kDsNonFinite);
   }
 }
@@ -256,7 +260,7 @@ template <bool F32, int U>
 __global__ __launch_bounds__(256) void k_f8_dequant(F8DequantArgs a, uint32_t units, uint32_t kb, uint32_t m, uint32_t mb) {
   constexpr int H = F32 ? 2 : 1, W = 8 / H;  // accesses per block, codes each
   const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const uint32_t first = (blockIdx.x * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
+  const uint32_t first = (group_index() * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
   uint32_t c[U][2], row[U];
   float G[U];
   int64_t col[U];
@@ -312,10 +316,12 @@ __global__ __launch_bounds__(256) void k_f8_dequant(F8DequantArgs a, uint32_t un
 
 // One 128 x 128 block of a matrix [m][K] to its place in [K][m].  Rows of 33 dwords in LDS: 16 rows x 8
 // dword columns, which a wave reads at once, fall into different banks.
-__global__ __launch_bounds__(256) void k_f8_transpose(F8TransposeArgs a, uint32_t mb, uint32_t kb) {
+__global__ __launch_bounds__(256) void k_f8_transpose(F8TransposeArgs a, uint32_t mb, uint32_t kb, uint32_t n) {
   __shared__ uint32_t tile[128 * 33];
   const int tid = threadIdx.x;
-  const uint32_t rest = blockIdx.x / kb, ct = blockIdx.x - rest * kb, s = rest / mb, rb = rest - s * mb;
+  const uint32_t block = group_index();
+  if (block >= n) return;  // uniform
+  const uint32_t rest = block / kb, ct = block - rest * kb, s = rest / mb, rb = rest - s * mb;
   const int64_t r0 = (int64_t)rb * 128, c0 = (int64_t)ct * 128;
   const uint8_t *src = a.codes + ((int64_t)s * a.m + r0) * a.K + c0;
 #pragma unroll
@@ -360,7 +366,7 @@ template <bool F32>
 hipError_t launch_rows(const F8QuantArgs &a, hipStream_t stream) {
   const int64_t kb = f8_blocks(a.K), units = a.rows * kb;
   const int u = f8_units_per_group(units);
-  const unsigned grid = (unsigned)((units + 16 * u - 1) / (16 * u));
+  const dim3 grid = many_groups((units + 16 * u - 1) / (16 * u));
   if (u == 4) k_f8_rows<F32, 4><<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)kb);
   else if (u == 2) k_f8_rows<F32, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)kb);
   else k_f8_rows<F32, 1><<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)kb);
@@ -374,21 +380,23 @@ hipError_t launch_f8_quantize(const F8QuantArgs &a, hipStream_t stream) {
   const int64_t kb = f8_blocks(a.K);
   if (a.layout == NV4_F8_TILES) {
     const int64_t m = a.rows / a.nseg, mb = f8_blocks(m);
-    const unsigned grid = (unsigned)(a.nseg * mb * kb);
-    if (a.x_is_f32) k_f8_tiles<true><<<grid, 512, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb, m);
-    else k_f8_tiles<false><<<grid, 256, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb, m);
+    const uint32_t n = (uint32_t)(a.nseg * mb * kb);
+    const dim3 grid = many_groups(n);
+    if (a.x_is_f32) k_f8_tiles<true><<<grid, 512, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb, m, n);
+    else k_f8_tiles<false><<<grid, 256, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb, m, n);
     return hipGetLastError();
   }
   // no more chunks than the rows can fill: every segment may have a ragged last one
   const int chunks = (int)std::min<int64_t>(a.out_K / 128, f8_blocks(a.rows) + a.nseg);
-  const unsigned grid = (unsigned)(chunks * kb);
+  const uint32_t n = (uint32_t)(chunks * kb);
+  const dim3 grid = many_groups(n);
   const bool both = a.layout == NV4_ROWS_AND_COLS;
   if (a.x_is_f32) {
-    if (both) k_f8_cols<true, true><<<grid, 512, 0, stream>>>(a, chunks);
-    else k_f8_cols<true, false><<<grid, 512, 0, stream>>>(a, chunks);
+    if (both) k_f8_cols<true, true><<<grid, 512, 0, stream>>>(a, chunks, n);
+    else k_f8_cols<true, false><<<grid, 512, 0, stream>>>(a, chunks, n);
   } else {
-    if (both) k_f8_cols<false, true><<<grid, 256, 0, stream>>>(a, chunks);
-    else k_f8_cols<false, false><<<grid, 256, 0, stream>>>(a, chunks);
+    if (both) k_f8_cols<false, true><<<grid, 256, 0, stream>>>(a, chunks, n);
+    else k_f8_cols<false, false><<<grid, 256, 0, stream>>>(a, chunks, n);
   }
   return hipGetLastError();
 }
@@ -397,7 +405,7 @@ hipError_t launch_f8_dequantize(const F8DequantArgs &a, hipStream_t stream) {
   const int64_t kb = f8_blocks(a.K), units = a.rows * kb;
   const int64_t m = a.nseg ? a.rows / a.nseg : 0, mb = f8_blocks(m);
   const int u = f8_units_per_group(units);
-  const unsigned grid = (unsigned)((units + 16 * u - 1) / (16 * u));
+  const dim3 grid = many_groups((units + 16 * u - 1) / (16 * u));
   const auto go = [&](auto f32, auto n) {
     k_f8_dequant<decltype(f32)::value, decltype(n)::value>
         <<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)kb, (uint32_t)m, (uint32_t)mb);
@@ -414,7 +422,8 @@ hipError_t launch_f8_dequantize(const F8DequantArgs &a, hipStream_t stream) {
 
 hipError_t launch_f8_transpose(const F8TransposeArgs &a, hipStream_t stream) {
   const int64_t mb = f8_blocks(a.m), kb = f8_blocks(a.K);
-  k_f8_transpose<<<(unsigned)(a.nseg * mb * kb), 256, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb);
+  const int64_t n = a.nseg * mb * kb;
+  k_f8_transpose<<<many_groups(n), 256, 0, stream>>>(a, (uint32_t)mb, (uint32_t)kb, (uint32_t)n);
   return hipGetLastError();
 }
 
