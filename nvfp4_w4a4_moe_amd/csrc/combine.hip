@@ -8,6 +8,7 @@
 // workgroup per token; every thread owns 4 consecutive columns (16-byte loads of
 // FP32 rows, 8-byte loads of BF16 rows); the k row indices and weights are
 // wave-uniform scalar loads.
+#include "many_groups.h"
 #include "nv4_device.h"
 #include "nv4_internal.h"
 
@@ -20,7 +21,8 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // KC > 0: k is the compile-time constant KC (all k row loads in flight together)
 template <bool Y_F32, bool OUT_F32, int KC>
 __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a) {
-  const int64_t t = blockIdx.x;
+  const int64_t t = group_index();
+  if (t >= a.T) return;
   const int k = KC > 0 ? KC : a.k;
   const int32_t *tr = a.token_row + t * k;
   const float *tw = a.topk_w + t * k;
@@ -62,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a) {
 
 template <int KC>
 void launch_k(const CombineArgs &a, hipStream_t stream) {
-  const unsigned grid = (unsigned)a.T;
+  const dim3 grid = many_groups(a.T);
   if (a.y_is_f32) {
     if (a.out_is_f32) k_combine<true, true, KC><<<grid, kThreads, 0, stream>>>(a);
     else k_combine<true, false, KC><<<grid, kThreads, 0, stream>>>(a);

@@ -23,6 +23,7 @@
 // do not hide.
 #include <algorithm>
 
+#include "many_groups.h"
 #include "mx_device.h"
 #include "mx_internal.h"
 #include "mx_rows.h"
@@ -45,7 +46,7 @@ __device__ __forceinline__ uint32_t clamp_row(const MxQuantArgs &a, int32_t i) {
 template <bool F32, int U>
 __global__ __launch_bounds__(256) void k_mx_rows(MxQuantArgs a, uint32_t units, uint32_t spr) {
   const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const uint32_t wave = group_index() * 4 + (threadIdx.x >> 6);
   const uint32_t first = wave * (4 * U) + (lane >> 4);
   uint4 v[U][F32 ? 2 : 1];
   uint32_t row[U], seg[U], src[U];
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQuantArgs a, uint32_t units, 
 // so a tile lies in one segment.  LDS row r keeps dword p of the tile at p ^ (16 * (r / 32 % 4)):
 // the four 32-row blocks that a wave's lanes read at once then fall into different banks.
 template <bool F32, bool BATCHED, bool ROWS>
-__global__ __launch_bounds__(256) void k_mx_cols(MxQuantArgs a, int chunks, int64_t m) {
+__global__ __launch_bounds__(256) void k_mx_cols(MxQuantArgs a, int chunks, int64_t m, uint32_t n) {
   constexpr int TC = F32 ? 64 : 128;
   __shared__ uint32_t tile[128 * 64];
   __shared__ int32_t s_seg[4];  // segment, its padded start, its rows
@@ -104,8 +105,9 @@ __global__ __launch_bounds__(256) void k_mx_cols(MxQuantArgs a, int chunks, int6
   // column tile for the column output (its 64-byte pieces); with gathered rows an XCD then reads
   // few columns of x, which its L2 keeps between the k copies of a token.  ROWS: two (FP32: four)
   // column tiles side by side, 128 bytes of a row's codes: 131072 x 2048 BF16 230 -> 203 us.
-  const uint32_t n = gridDim.x, per = n / kXcds, full = per * kXcds;
-  const uint32_t L = blockIdx.x < full ? (blockIdx.x % kXcds) * per + blockIdx.x / kXcds : blockIdx.x;
+  const uint32_t b0 = group_index(), per = n / kXcds, full = per * kXcds;
+  if (b0 >= n) return;  // uniform
+  const uint32_t L = b0 < full ? (b0 % kXcds) * per + b0 / kXcds : b0;
   constexpr uint32_t G = ROWS ? 256 / TC : 1;
   const uint32_t g0 = L / (G * chunks) * G, gw = min(G, n / chunks - g0), in = L - g0 * chunks;
   const uint32_t ch = in / gw, ct = g0 + in - ch * gw;
@@ -282,7 +284,7 @@ template <bool F32, int U>
 __global__ __launch_bounds__(256) void k_mx_dequant(MxDequantArgs a, uint32_t units, uint32_t spr) {
   constexpr int H = F32 ? 2 : 1, W = 8 / H;  // accesses per unit, codes each
   const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const uint32_t first = (blockIdx.x * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
+  const uint32_t first = (group_index() * 4 + (threadIdx.x >> 6)) * (4 * U) + (lane >> 4);
   const int64_t sld = (a.K / kMxBlock + 3) / 4 * 4;
   uint32_t c[U][H], row[U], d[U];
   int64_t col[U];
@@ -359,7 +361,7 @@ void launch_rows(const MxQuantArgs &a, hipStream_t stream) {
   // units one each spreads them wider.
   const bool many = units >= (int64_t)device_cu_count() * 64;
   const unsigned per = many ? 32 : 16;
-  const unsigned grid = (unsigned)((units + per - 1) / per);
+  const dim3 grid = many_groups((units + per - 1) / per);
   if (many) k_mx_rows<F32, 2><<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)spr);
   else k_mx_rows<F32, 1><<<grid, 256, 0, stream>>>(a, (uint32_t)units, (uint32_t)spr);
 }
@@ -371,15 +373,17 @@ void launch_cols(const MxQuantArgs &a, hipStream_t stream) {
   const int64_t ctiles = (a.K + 127) / 128 * (128 / TC);
   if (a.layout == NV4_COLS_BATCHED) {
     const int64_t m = a.rows / a.nseg, chunks = a.nseg * ((m + 127) / 128);
-    k_mx_cols<F32, true, false><<<(unsigned)(ctiles * chunks), 256, 0, stream>>>(a, (int)chunks, m);
+    const int64_t n = ctiles * chunks;
+    k_mx_cols<F32, true, false><<<many_groups(n), 256, 0, stream>>>(a, (int)chunks, m, (uint32_t)n);
     return;
   }
   // every segment ends at most 127 columns of padding behind its rows
   const int64_t chunks = std::min(a.out_K / 128, (a.rows + 127 * (int64_t)a.nseg) / 128);
   if (chunks == 0) return;
-  const unsigned grid = (unsigned)(ctiles * chunks);
-  if (a.layout == NV4_COLS) k_mx_cols<F32, false, false><<<grid, 256, 0, stream>>>(a, (int)chunks, 0);
-  else k_mx_cols<F32, false, true><<<grid, 256, 0, stream>>>(a, (int)chunks, 0);
+  const uint32_t n = (uint32_t)(ctiles * chunks);
+  const dim3 grid = many_groups(n);
+  if (a.layout == NV4_COLS) k_mx_cols<F32, false, false><<<grid, 256, 0, stream>>>(a, (int)chunks, 0, n);
+  else k_mx_cols<F32, false, true><<<grid, 256, 0, stream>>>(a, (int)chunks, 0, n);
 }
 
 }  // namespace
@@ -399,7 +403,7 @@ hipError_t launch_mx_dequantize(const MxDequantArgs &a, hipStream_t stream) {
   const int64_t spr = (a.K + 127) / 128, units = a.rows * spr;
   const bool many = units >= (int64_t)device_cu_count() * 64;
   const unsigned per = many ? 32 : 16;
-  const unsigned grid = (unsigned)((units + per - 1) / per);
+  const dim3 grid = many_groups((units + per - 1) / per);
   const uint32_t n = (uint32_t)units, s = (uint32_t)spr;
   if (a.out_is_f32) {
     if (many) k_mx_dequant<true, 2><<<grid, 256, 0, stream>>>(a, n, s);

@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "many_groups.h"
 #include "nv4_device.h"
 #include "nv4_internal.h"
 #include "topk_device.h"
@@ -37,7 +38,7 @@ __global__ __launch_bounds__(256) void k_topk(PermuteArgs a) {
   constexpr int TPW = kWave / LPT;  // tokens per wave
   const int lane = threadIdx.x & 63;
   const int sub = lane / LPT, ll = lane % LPT;
-  const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * TPW;
+  const int64_t t0 = ((int64_t)group_index() * 4 + (threadIdx.x >> 6)) * TPW;
   if (t0 >= a.T) return;  // uniform over the wave
   const int64_t t = t0 + sub;
   const bool valid = t < a.T;  // the second token of the last wave may not exist
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(256) void k_scatter(PermuteArgs a) {
 // one wave per permuted row: copy the packed codes and scale bytes of its token
 __global__ __launch_bounds__(256) void k_gather(PermuteArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t r = (int64_t)group_index() * 4 + (threadIdx.x >> 6);
   const int64_t R = a.T * a.k;
   if (r >= R) return;
   const int64_t t = a.row_token[r];
@@ -228,7 +229,7 @@ hipError_t launch_permute(const PermuteArgs &a, hipStream_t stream) {
   while ((1 << nbits) < a.E) ++nbits;
   if (a.logits) {
     // four waves per workgroup; two tokens per wave up to 128 experts (k <= 32 <= LPT)
-    const unsigned g1 = (unsigned)((a.T + 3) / 4), g2 = (unsigned)((a.T + 7) / 8);
+    const dim3 g1 = many_groups((a.T + 3) / 4), g2 = many_groups((a.T + 7) / 8);
     if (a.E <= 64) k_topk<2, 32><<<g2, 256, 0, stream>>>(a);
     else if (a.E <= 128) k_topk<4, 32><<<g2, 256, 0, stream>>>(a);
     else if (a.E <= 256) k_topk<4, 64><<<g1, 256, 0, stream>>>(a);
@@ -239,7 +240,7 @@ hipError_t launch_permute(const PermuteArgs &a, hipStream_t stream) {
   k_scan_chunks<<<a.E, 64, 0, stream>>>(a, nchunks);
   k_scan_experts<<<1, 1024, 0, stream>>>(a, 1);
   k_scatter<<<(unsigned)((R + 255) / 256), 256, 0, stream>>>(a);
-  if (a.gather_K > 0) k_gather<<<(unsigned)((R + 3) / 4), 256, 0, stream>>>(a);
+  if (a.gather_K > 0) k_gather<<<many_groups((R + 3) / 4), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
