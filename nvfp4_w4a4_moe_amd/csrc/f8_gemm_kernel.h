@@ -515,8 +515,8 @@ void k_f8_gemm(F8GemmArgs g) {
 
   // ---- products
   // A fragment pair's sum over the block goes onto the accumulators under the block's scales: while the
-  // SIMD's other wave multiplies, or, where the registers last for it, from one of two buffers under its own next
-  // pair's products as well (8192^3 with FP32 results 997 -> 940 us).
+  // SIMD's other wave multiplies, or, for FP32 results of up to four pairs, whose products take twice as long, from one of
+  // two buffers under its own next pair's products as well (8192^3 with FP32 results 997 -> 940 us).
   constexpr int NP = OUT_F32 && !MANY && FM * FN <= 4 ? 2 : 1;
   f32x16 p[NP];
   float ps = 0.0f;  // the waiting sum's scale

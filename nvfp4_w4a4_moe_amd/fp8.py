@@ -172,7 +172,8 @@ def fp8_grouped_gemm(A: FP8, B: FP8, offsets: torch.Tensor, E: int, N: int, M_ca
                      rule: int = NV4_F8_FP32, want_c: bool = True, stream=None) -> torch.Tensor | None:
     """GROUP_M: C [M_cap, N] = per-expert A_e . B_e^T (SwiGLU: N output columns from 2N rows of
     B per expert).  GROUP_K: C [E, A.rows, B.rows] over per-expert K ranges.  q_out (SwiGLU):
-    also the FP8 form of the result under `rule`; with want_c=False that alone."""
+    also the FP8 form of the result under `rule`; with want_c=False that alone.  A block of q_out that is not
+    finite has the scale NaN (there is no dev_status)."""
     call = _Call(stream, A.codes, A.scales, B.codes, B.scales, offsets, a_rows, C, q_out and q_out.codes,
                  q_out and q_out.scales)
     if group_mode == NV4_GROUP_K:
@@ -272,7 +273,8 @@ def fp8_moe_forward(x: torch.Tensor, logits: torch.Tensor, w: F8ExpertWeights, k
                     bufs: F8ForwardBuffers | None = None, flags: int = 0, stream=None,
                     stage_events: list | None = None) -> F8ForwardBuffers:
     """One FP8 expert-layer forward: quantise x, route and permute, gate and up products with
-    SwiGLU and re-quantisation in the epilogue, down product, combine (``out``)."""
+    SwiGLU and re-quantisation in the epilogue, down product, combine (``out``).  As the other layers it takes no
+    dev_status: NaN and infinity of x show as NaN in their tokens' rows of out."""
     T, H = x.shape
     R = T * k
     if H != w.H:
@@ -337,7 +339,8 @@ def fp8_moe_backward(x: torch.Tensor, fwd: F8ForwardBuffers, wt: F8TransposedWei
     """The four backward grouped GEMMs of ``moe_backward`` on FP8 operands: gradients and activations
     quantised along their contraction dimension, the forward's weights transposed.  dY2 [R, H]
     and dY13 [R, 2I] are the gradients of the down and the gate/up output rows in expert (permuted)
-    row order; the forward kept its SwiGLU output (keep_hact)."""
+    row order; the forward kept its SwiGLU output (keep_hact).  SwiGLU's own gradient, which makes dY13 from
+    dhact and the gate and up rows, is the caller's, as in the other layers."""
     if fwd.hact is None:
         raise ValueError("the forward kept no SwiGLU output: fp8_alloc_forward(keep_hact=True)")
     T, H = x.shape
