@@ -131,10 +131,9 @@ def fp8_quantize(x: torch.Tensor, layout: int = NV4_ROWS, nseg: int = 1, seg_off
     scaled = nseg if tiles else 0
     call(load().fp8_quantize, x.data_ptr(), _float(x, "x"), x.shape[0], rows, K, ldx, ri, layout, nseg, so, sp, rule,
          out.c(scaled), None if out_rows is None else out_rows.c(0), ds)
-    out.nseg, out.rule = scaled, rule
+    out.nseg, out.rule, out.rows_out = scaled, rule, out_rows
     if out_rows is not None:
-        out_rows.nseg, out_rows.rule = 0, rule
-        out.rows_out = out_rows
+        out_rows.nseg, out_rows.rule, out_rows.rows_out = 0, rule, None
     return out
 
 
@@ -160,7 +159,7 @@ def fp8_transpose(q: FP8, out: FP8 | None = None, stream=None) -> FP8:
     if out is None:
         out = _new(call, q.nseg * q.K, q.rows // q.nseg, q.nseg)
     call(load().fp8_transpose, q.c(), out.c(q.nseg))
-    out.nseg, out.rule = q.nseg, q.rule
+    out.nseg, out.rule, out.rows_out = q.nseg, q.rule, None
     return out
 
 
@@ -202,7 +201,7 @@ def fp8_grouped_gemm(A: FP8, B: FP8, offsets: torch.Tensor, E: int, N: int, M_ca
          None if a_rows is None else _ints(a_rows, "a_rows"), group_mode, epilogue, _p(C), ctype, ldc,
          None if q_out is None else q_out.c(0), rule)
     if q_out is not None:
-        q_out.nseg, q_out.rule = 0, rule
+        q_out.nseg, q_out.rule, q_out.rows_out = 0, rule, None
     return C
 
 

@@ -242,8 +242,7 @@ def mxfp4_quantize(x: torch.Tensor, layout: int = NV4_ROWS, nseg: int = 1, seg_o
         out_rows = call.mx(rows, K)
     call(load().mxfp4_quantize, x.data_ptr(), _float(x, "x"), x.shape[0], rows, K, ldx, ri, layout, nseg, so, sp, rule,
          c, None if out_rows is None else out_rows.c(), ds)
-    if out_rows is not None:
-        out.rows_out = out_rows
+    out.rows_out = out_rows
     return out
 
 
