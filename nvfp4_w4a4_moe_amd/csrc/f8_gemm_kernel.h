@@ -28,8 +28,8 @@
 // slot just read is refilled.  Every stage issues the same number of loads (a load with nothing to fetch has
 // an offset behind the buffer), so a wait counts exactly what may still be under way.
 //
-// 8192^3: 527 us or 2085 TFLOP/s (by the clock, 1970 to 2090), power-of-two scales 2130 to 2200, FP32 results 1185.  Gate
-// and up of 131072 rows with SwiGLU (128 experts, K 2048, 768 columns): 436 us, 1890 TFLOP/s.  What bounds it: MFMA is
+// 8192^3: 550 us or 1990 TFLOP/s, power-of-two scales 2090, FP32 results 1170.  Gate and up of 131072 rows with SwiGLU
+// (128 experts, K 2048, 768 columns): 444 to 454 us, 1830 TFLOP/s.  What bounds it: MFMA is
 // busy 44 % of the cycles, the VALU (the sums' multiply-adds, addresses) 45 %, hardly both at once, and LDS reads 24
 // KB for 16 MFMA of a wave, as long as they take.
 #pragma once
@@ -77,7 +77,8 @@ struct F8Tile {
 // nothing else in these kernels uses (the compiler takes it for its own: it can't be named as clobbered).
 // A buffer load may read a scalar register five wait states after a vector instruction has written it, and the
 // operands here often come straight from a lane read, where scalars are kept: the compiler puts such waits before loads
-// of its own only, so m0's move and the nop are five.
+// of its own only, so m0's move and the nop are five (8192 x 2048 x 768 22.1 -> 22.9 us, 131072 rows of gate and up 436 ->
+// 444).
 __device__ __forceinline__ i32x4 f8_buffer(const void *base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   return i32x4{(int)p, (int)(p >> 32) & 0xFFFF, (int)bytes, 0x00020000};
