@@ -1,4 +1,5 @@
-"""The same for the calls that those go with: the combine, the routing and the MXFP4 conversions."""
+"""Calls of more work than one dimension of a launch counts (2^32 work-items): the combine, the routing and the MXFP4
+conversions at sizes that their contracts allow."""
 
 import numpy as np
 import pytest
